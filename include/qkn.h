@@ -445,6 +445,83 @@ QKN_EXPORT qkn_status qkn_gqa_decode(const qkn_dims* dims, const qkn_gqa_cache* 
                       int32_t s_q, const int32_t* selection, int32_t sel_k, void* workspace, size_t ws_bytes,
                       void* out_v, float* lse, int32_t max_ctas, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit projections around the decode: hidden states to the inputs of
+ * qkn_append and qkn_absorb_query (q, q^R, c, k^R), and the attention output
+ * back to hidden states.  Activations are quantised row by row, weights once
+ * when a model is loaded, both to e4m3 with one fp32 scale for each block of
+ * 128; the product keeps fp32 sums.  The pages leave the projections to the
+ * surrounding model; these calls are this library's.
+ * ------------------------------------------------------------------------- */
+
+/* Rows in 8 bits: element (i, j) stands for codes[i * ld + j] * scale[(j / 128) * ld_scale + i].
+ *   codes [rows, ld] e4m3, 16-byte aligned; ld >= cols, a multiple of 16
+ *   scale [ceil(cols / 128), ld_scale] fp32, 16-byte aligned; ld_scale >= rows, a multiple of 4
+ * (one row of scales per block of columns, so that the product reads the
+ * scales of a tile's rows as one piece).  What lies behind a row's `cols`
+ * codes and behind the `rows` scales of a block is neither read nor written. */
+typedef struct {
+  void* codes;
+  float* scale;
+  int32_t rows, cols;
+  int64_t ld, ld_scale;
+} qkn_fp8_rows;
+
+/* A weight in 8 bits, one row per output column: element (n, k) stands for
+ * codes[n * ld + k] * scale[(n / 128) * ceil(cols / 128) + k / 128].
+ *   codes [rows, ld] e4m3, 16-byte aligned; ld >= cols, a multiple of 16
+ *   scale [ceil(rows / 128), ceil(cols / 128)] fp32 */
+typedef struct {
+  void* codes;
+  float* scale;
+  int32_t rows, cols;
+  int64_t ld;
+} qkn_fp8_weight;
+
+/* A run of consecutive output columns of qkn_fp8_linear and where they go: out[i * ld + j], any alignment of the
+ * element type; ld >= cols. */
+typedef struct {
+  void* out;
+  int32_t cols;
+  int64_t ld;
+} qkn_out_cols;
+
+#define QKN_MAX_OUTS 8
+
+/* qkn_norm_quant — residual addition, RMSNorm and quantisation of n = q->rows rows of d = q->cols values:
+ *   h = x, or x + residual rounded to dtype and written to residual_out;
+ *   y = h * gamma / sqrt(mean(h^2) + eps), or y = h without gamma (no norm);
+ *   per row and block of 128 columns: scale = max(max|y| / 448, 2^-100), code = y / scale rounded to
+ *   the nearest e4m3 (ties to even).
+ * fp32 arithmetic; the sum of squares must stay in fp32's range.  A NaN makes its block of codes (with
+ * gamma: its row) NaN, an infinity without gamma its block; other rows are not touched by it.
+ *   x         [n, ld_x] dtype, ld_x >= d;  residual, residual_out [n, d] dtype, both or neither
+ *   gamma     [d] fp32 or NULL;  y [n, d] dtype or NULL: the normalised rows, rounded to dtype
+ *   residual_out may be residual, or x where ld_x = d; y may be x where ld_x = d and residual is NULL
+ * rows == 0 is a no-op.  Any d; rows that are 16-byte aligned throughout with d a multiple of 8 and at
+ * most 32768 are read once.  Returns QKN_ERR_INVALID_ARG for a bad size, pointer or alignment. */
+QKN_EXPORT qkn_status qkn_norm_quant(qkn_dtype dtype, const void* x, int64_t ld_x, const void* residual,
+                      const float* gamma, float eps, void* residual_out, void* y, const qkn_fp8_rows* q,
+                      void* stream);
+
+/* qkn_quant_weight — quantise a weight [q->rows, q->cols] (row-major, dense) of type dtype: per block of 128 x 128
+ * scale = max(max|w| / 448, 2^-100), code = w / scale rounded to the nearest e4m3.  A NaN or an infinity makes its
+ * block NaN. */
+QKN_EXPORT qkn_status qkn_quant_weight(qkn_dtype dtype, const void* w, const qkn_fp8_weight* q, void* stream);
+
+/* qkn_fp8_linear — out = A W^T for rows and a weight in 8 bits:
+ *   out[i, n] = sum over blocks b of scale_a[b, i] scale_w[n / 128, b] sum_{k in b} a[i, k] w[n, k],
+ * products and sums in fp32, rounded once to out_dtype.  The columns go to n_outs <= QKN_MAX_OUTS
+ * destinations in order (their widths add up to w->rows), so that one product fills, say, q, q^R, c and
+ * k^R where qkn_append_absorb reads them.
+ *   a->cols == w->cols;  workspace >= 256 bytes, 256-byte aligned, initialised with qkn_workspace_init:
+ *   its status word records a bounded wait that ran out (QKN_ERR_TIMEOUT; the outputs are then not
+ *   valid).  Calls that overlap may share it.
+ * a->rows == 0 is a no-op.  The outputs must not overlap each other or the inputs.  Returns
+ * QKN_ERR_INVALID_ARG for bad sizes, pointers, alignment or widths. */
+QKN_EXPORT qkn_status qkn_fp8_linear(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dtype out_dtype,
+                      int32_t n_outs, const qkn_out_cols* outs, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, then read the workspace status word into *device_status
  * (a qkn_status value; QKN_OK if no kernel recorded an error).  The word is
  * sticky until qkn_workspace_init clears it. */

@@ -48,6 +48,11 @@ The GQA route's pins: equality with the absorbed route over group-tied
 weights; torch's grouped-query attention on keys and values the check forms;
 a one-token closed form; a full selection equal to dense and an empty one
 giving zeros; a brute-force loop over a sparse selection.
+The 8-bit projections (blocks of 128 that share an fp32 scale) are here by their definitions:
+the e4m3 grid enumerated from its bit patterns, the nearest value by search, scales from a
+block's largest magnitude, the product over the values that codes and scales stand for.
+Their pins: torch's e4m3 conversion over every midpoint; codes within half a step; exact
+rational products on a small case.
 The absolute outputs on the workloads are parity unpinned beyond those
 properties: the pages print no worked example.
 """
@@ -60,7 +65,8 @@ import numpy as np
 __all__ = ["inv_rms", "rms_norm", "rope", "key_inv_rms", "rope_keys", "absorbed_query",
            "sequence_logits", "decode", "decode_sequence", "up_project", "group_keys",
            "group_values",
-           "gqa_logits", "gqa_decode_sequence", "gqa_decode"]
+           "gqa_logits", "gqa_decode_sequence", "gqa_decode",
+           "e4m3_values", "e4m3_round", "quant_rows", "quant_weight", "row_values", "weight_values", "fp8_linear"]
 
 
 def inv_rms(x: np.ndarray, eps: float) -> np.ndarray:
@@ -336,3 +342,69 @@ def gqa_decode(inp, w_uk: np.ndarray, gamma_k: np.ndarray, w_uv: np.ndarray,
         o[b], lse[b] = gqa_decode_sequence(inp, b, w_uk, gamma_k, w_uv,
                                            None if selection is None else selection[b])
     return o, lse
+
+
+# ---------------------------------------------------------------- the 8-bit projections
+FP8_GROUP = 128
+FP8_TOP = 448.0
+FP8_LEAST = 2.0 ** -100
+
+
+def e4m3_values() -> np.ndarray:
+    """The non-negative finite e4m3 values in order, from the bit patterns (4 exponent bits of bias 7,
+    3 fraction bits, no infinity, all ones NaN)."""
+    out = []
+    for bits in range(0x7F):
+        e, f = bits >> 3, bits & 7
+        out.append((f / 8.0) * 2.0 ** -6 if e == 0 else (1 + f / 8.0) * 2.0 ** (e - 7))
+    return np.array(out)
+
+
+def e4m3_round(x: np.ndarray) -> np.ndarray:
+    """The nearest e4m3 value (ties to the even bit pattern); magnitudes above 448 become 448, NaN stays."""
+    x = np.asarray(x, dtype=np.float64)
+    grid = e4m3_values()
+    mag = np.minimum(np.abs(np.nan_to_num(x, nan=0.0)), FP8_TOP)
+    hi = np.clip(np.searchsorted(grid, mag), 1, len(grid) - 1)
+    lo = hi - 1
+    below, above = mag - grid[lo], grid[hi] - mag
+    pick = np.where((below < above) | ((below == above) & (lo % 2 == 0)), lo, hi)
+    return np.where(np.isnan(x), np.nan, np.copysign(grid[pick], x))
+
+
+def quant_rows(y: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """Rows [n, d] -> (y / scale before rounding [n, d], scale [ceil(d / 128), n])."""
+    y = np.asarray(y, dtype=np.float64)
+    n, d = y.shape
+    scale = np.stack([np.abs(y[:, j:j + FP8_GROUP]).max(axis=1) / FP8_TOP for j in range(0, d, FP8_GROUP)])
+    scale = np.maximum(scale, FP8_LEAST)
+    return y / scale[np.arange(d) // FP8_GROUP].T, scale
+
+
+def quant_weight(w: np.ndarray) -> Tuple[np.ndarray, np.ndarray]:
+    """A weight [n, k] -> (w / scale before rounding, scale [ceil(n / 128), ceil(k / 128)])."""
+    w = np.asarray(w, dtype=np.float64)
+    n, k = w.shape
+    scale = np.array([[np.abs(w[i:i + FP8_GROUP, j:j + FP8_GROUP]).max() / FP8_TOP for j in range(0, k, FP8_GROUP)]
+                      for i in range(0, n, FP8_GROUP)])
+    scale = np.maximum(scale, FP8_LEAST)
+    return w / scale[np.arange(n) // FP8_GROUP][:, np.arange(k) // FP8_GROUP], scale
+
+
+def row_values(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
+    """What rows in 8 bits stand for: codes [n, d], scale [ceil(d / 128), >= n]."""
+    codes = np.asarray(codes, dtype=np.float64)
+    n, d = codes.shape
+    return codes * np.asarray(scale, dtype=np.float64)[np.arange(d) // FP8_GROUP, :n].T
+
+
+def weight_values(codes: np.ndarray, scale: np.ndarray) -> np.ndarray:
+    """What a weight in 8 bits stands for: codes [n, k], scale [ceil(n / 128), ceil(k / 128)]."""
+    codes = np.asarray(codes, dtype=np.float64)
+    n, k = codes.shape
+    return codes * np.asarray(scale, dtype=np.float64)[np.arange(n) // FP8_GROUP][:, np.arange(k) // FP8_GROUP]
+
+
+def fp8_linear(a_codes, a_scale, w_codes, w_scale) -> np.ndarray:
+    """out = A W^T over the values the codes stand for."""
+    return row_values(a_codes, a_scale) @ weight_values(w_codes, w_scale).T

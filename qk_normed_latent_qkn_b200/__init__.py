@@ -27,7 +27,10 @@ KERNEL_AUTO, KERNEL_SIMT, KERNEL_TCGEN05 = 0, 1, 2
 EXPORTED = ["qkn_append", "qkn_absorb_query", "qkn_decode_workspace_size", "qkn_workspace_init",
             "qkn_decode", "qkn_read_device_status", "qkn_decode_kernel_for", "qkn_status_string",
             "qkn_version", "qkn_decode_noalloc", "qkn_append_absorb", "qkn_key_gram", "qkn_decode_up",
-            "qkn_merge_partials", "qkn_gqa_append", "qkn_gqa_workspace_size", "qkn_gqa_decode"]
+            "qkn_merge_partials", "qkn_gqa_append", "qkn_gqa_workspace_size", "qkn_gqa_decode",
+            "qkn_norm_quant", "qkn_quant_weight", "qkn_fp8_linear"]
+MAX_OUTS = 8               # destinations of one fp8_linear
+WORKSPACE_BYTES = 256      # what fp8_linear needs of a workspace (the status word)
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -54,6 +57,20 @@ class _GqaCache(ctypes.Structure):
                 ("num_blocks", ctypes.c_int32), ("d_v", ctypes.c_int32)]
 
 
+class _Fp8Rows(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("ld", ctypes.c_int64), ("ld_scale", ctypes.c_int64)]
+
+
+class _Fp8Weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("cols", ctypes.c_int32), ("ld", ctypes.c_int64)]
+
+
+class _OutCols(ctypes.Structure):
+    _fields_ = [("out", ctypes.c_void_p), ("cols", ctypes.c_int32), ("ld", ctypes.c_int64)]
+
+
 class _Opts(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("max_ctas", ctypes.c_int32), ("head_tile", ctypes.c_int32),
                 ("wait_limit", ctypes.c_int64), ("split_event", ctypes.c_void_p),
@@ -68,6 +85,7 @@ def _load() -> ctypes.CDLL:
     P, I32, I64, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     PD, PC, PO = ctypes.POINTER(_Dims), ctypes.POINTER(_Cache), ctypes.POINTER(_Opts)
     PG = ctypes.POINTER(_GqaCache)
+    PR, PW, PU = ctypes.POINTER(_Fp8Rows), ctypes.POINTER(_Fp8Weight), ctypes.POINTER(_OutCols)
     sig = {
         "qkn_append": (I32, [PD, PC, P, P, P, P, I32, P, P, P, P]),
         "qkn_key_gram": (I32, [PD, P, P, P]),
@@ -86,6 +104,9 @@ def _load() -> ctypes.CDLL:
         "qkn_gqa_append": (I32, [PD, PG, P, P, P, P, I32, P, P, P, P, P]),
         "qkn_gqa_workspace_size": (I32, [PD, I32, I32, I32, I32, ctypes.POINTER(SZ)]),
         "qkn_gqa_decode": (I32, [PD, PG, P, P, P, P, P, I32, P, I32, I32, P, I32, P, SZ, P, P, I32, P]),
+        "qkn_norm_quant": (I32, [I32, P, I64, P, P, ctypes.c_float, P, P, PR, P]),
+        "qkn_quant_weight": (I32, [I32, P, PW, P]),
+        "qkn_fp8_linear": (I32, [PR, PW, I32, I32, PU, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -317,6 +338,126 @@ def gqa_decode(dims: Dims, cache: GqaCache, q, q_rope, gamma_q, gamma_qr, block_
                                _ptr(gamma_qr), _ptr(block_table), max_blocks, _ptr(seq_lens), batch, s_q,
                                _ptr(selection), sel_k, _ptr(workspace), workspace.numel() * workspace.element_size(),
                                _ptr(out_v), _ptr(lse), max_ctas, _stream(stream)), "qkn_gqa_decode")
+
+
+# ----------------------------------------------------------------- 8-bit projections
+FP8_GROUP = 128            # columns (and, in a weight, rows) that share a scale
+
+
+def _round_up(v: int, to: int) -> int:
+    return (v + to - 1) // to * to
+
+
+class Fp8Rows:
+    """Rows of ``cols`` values in 8 bits (see qkn_fp8_rows): ``codes`` float8_e4m3fn [rows, ld], ``scale`` fp32
+    [ceil(cols / 128), ld_scale] with a block's scales of all rows side by side."""
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, cols: int):
+        _need(codes.dim() == 2 and codes.dtype == torch.float8_e4m3fn and codes.is_contiguous(),
+              "codes is a contiguous float8_e4m3fn [rows, ld]")
+        _need(scale.dim() == 2 and scale.dtype == torch.float32 and scale.is_contiguous(),
+              "scale is a contiguous float32 [ceil(cols / 128), ld_scale]")
+        _need(1 <= cols <= codes.shape[1] and scale.shape[0] == (cols + FP8_GROUP - 1) // FP8_GROUP
+              and scale.shape[1] >= codes.shape[0] and scale.device == codes.device,
+              "codes and scale hold rows of cols values, on one device")
+        self.codes, self.scale, self.rows, self.cols = codes, scale, int(codes.shape[0]), int(cols)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda") -> "Fp8Rows":
+        return cls(torch.empty((rows, _round_up(cols, 16)), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(((cols + FP8_GROUP - 1) // FP8_GROUP, max(4, _round_up(rows, 4))),
+                               dtype=torch.float32, device=device), cols)
+
+    def c(self) -> _Fp8Rows:
+        return _Fp8Rows(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.codes.shape[1],
+                        self.scale.shape[1])
+
+
+class Fp8Weight:
+    """A weight in 8 bits, one row per output column (see qkn_fp8_weight): ``codes`` float8_e4m3fn [rows, ld],
+    ``scale`` fp32 [ceil(rows / 128), ceil(cols / 128)]."""
+
+    def __init__(self, codes: torch.Tensor, scale: torch.Tensor, cols: int):
+        _need(codes.dim() == 2 and codes.dtype == torch.float8_e4m3fn and codes.is_contiguous(),
+              "codes is a contiguous float8_e4m3fn [rows, ld]")
+        _need(1 <= cols <= codes.shape[1] and scale.dtype == torch.float32 and scale.is_contiguous()
+              and scale.device == codes.device
+              and tuple(scale.shape) == ((codes.shape[0] + FP8_GROUP - 1) // FP8_GROUP,
+                                         (cols + FP8_GROUP - 1) // FP8_GROUP),
+              "scale is a contiguous float32 [ceil(rows / 128), ceil(cols / 128)] on the codes' device")
+        self.codes, self.scale, self.rows, self.cols = codes, scale, int(codes.shape[0]), int(cols)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda") -> "Fp8Weight":
+        return cls(torch.empty((rows, _round_up(cols, 16)), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty(((rows + FP8_GROUP - 1) // FP8_GROUP, (cols + FP8_GROUP - 1) // FP8_GROUP),
+                               dtype=torch.float32, device=device), cols)
+
+    def c(self) -> _Fp8Weight:
+        return _Fp8Weight(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.codes.shape[1])
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _dtype_code(t: torch.Tensor, what: str) -> int:
+    _need(t.dtype in (torch.bfloat16, torch.float32), f"{what} is bfloat16 or float32")
+    return BF16 if t.dtype == torch.bfloat16 else F32
+
+
+def _call_on(device: torch.device, stream, call) -> int:
+    """``call(stream handle)`` with ``device`` current: the library launches on the current device."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def norm_quant(x, q: Fp8Rows, gamma=None, eps: float = 1e-6, residual=None, residual_out=None, y=None,
+               stream=None) -> None:
+    """Residual addition, RMSNorm (with ``gamma``) and quantisation of rows to 8 bits (see qkn_norm_quant): ``x``
+    [n, d], its rows contiguous; ``residual`` / ``residual_out`` / ``y`` dense [n, d] of x's type or None."""
+    _need(x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] == 1), "x is [n, d] with contiguous rows")
+    n, d = int(x.shape[0]), int(x.shape[1])
+    _need((q.rows, q.cols) == (n, d), "q holds n rows of d values")
+    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (y, "y")):
+        _need(t is None or (t.dtype == x.dtype and tuple(t.shape) == (n, d) and t.is_contiguous()
+                            and t.device == x.device), f"{what} is a dense [n, d] of x's type and device")
+    _need(gamma is None or (gamma.dtype == torch.float32 and tuple(gamma.shape) == (d,) and gamma.is_contiguous()
+                            and gamma.device == x.device), "gamma is a float32 [d] on x's device")
+    _need(q.codes.device == x.device, "q is on x's device")
+    ld_x = int(x.stride(0)) if n > 1 else d
+    _check(_call_on(x.device, stream, lambda st: _lib.qkn_norm_quant(
+        _dtype_code(x, "x"), _ptr(x), ld_x, _ptr(residual), _ptr(gamma), eps, _ptr(residual_out), _ptr(y),
+        ctypes.byref(q.c()), st)), "qkn_norm_quant")
+
+
+def quant_weight(w, q: Fp8Weight, stream=None) -> None:
+    """Quantise a dense weight [n, k] to 8 bits with a scale for each block of 128 x 128 (see qkn_quant_weight)."""
+    _need(w.dim() == 2 and w.is_contiguous() and (q.rows, q.cols) == tuple(w.shape) and q.codes.device == w.device,
+          "w is a dense [n, k], q holds as much on its device")
+    _check(_call_on(w.device, stream, lambda st: _lib.qkn_quant_weight(_dtype_code(w, "w"), _ptr(w),
+                                                                       ctypes.byref(q.c()), st)), "qkn_quant_weight")
+
+
+def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=None) -> None:
+    """out = A W^T from 8 bits (see qkn_fp8_linear); ``outs``: up to MAX_OUTS tensors [a.rows, width] of one type,
+    their rows contiguous, that take the product's columns in order."""
+    _need(1 <= len(outs) <= MAX_OUTS, f"outs holds 1 to {MAX_OUTS} tensors")
+    dev = a.codes.device
+    arr = (_OutCols * len(outs))()
+    for i, t in enumerate(outs):
+        _need(t.dim() == 2 and t.shape[0] == a.rows and (t.stride(1) == 1 or t.shape[1] == 1)
+              and t.dtype == outs[0].dtype and t.device == dev,
+              "an output is [rows, width] with contiguous rows, all of one type, on the codes' device")
+        width = int(t.shape[1])
+        arr[i] = _OutCols(t.data_ptr(), width, int(t.stride(0)) if a.rows > 1 else width)
+    _need(w.codes.device == dev and workspace.device == dev, "all tensors are on one device")
+    _check(_call_on(dev, stream, lambda st: _lib.qkn_fp8_linear(
+        ctypes.byref(a.c()), ctypes.byref(w.c()), _dtype_code(outs[0], "outs"), len(outs), arr, _ptr(workspace),
+        workspace.numel() * workspace.element_size(), st)), "qkn_fp8_linear")
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:

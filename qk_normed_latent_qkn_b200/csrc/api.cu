@@ -676,3 +676,105 @@ qkn_status qkn_gqa_decode(const qkn_dims* dims, const qkn_gqa_cache* cache, cons
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- the 8-bit projections
+
+namespace {
+
+bool check_dtype(qkn_dtype t) { return t == QKN_F32 || t == QKN_BF16; }
+
+// Codes and scales of `rows` rows of `cols` values each (a weight's scales are dense, ld_scale = 0 here).
+bool check_fp8(const void* codes, const float* scale, int32_t rows, int32_t cols, int64_t ld, int64_t ld_scale) {
+  if (rows < 0 || cols < 1 || ld < cols || ld % 16 || ld > (int64_t{1} << 32)) return false;
+  if ((rows > 0 && (!codes || !scale)) || !aligned(codes, 16)) return false;
+  if (ld_scale == 0) return aligned(scale, 4);
+  return ld_scale >= rows && ld_scale % 4 == 0 && ld_scale <= (int64_t{1} << 32) && aligned(scale, 16);
+}
+
+}  // namespace
+
+extern "C" {
+
+qkn_status qkn_norm_quant(qkn_dtype dtype, const void* x, int64_t ld_x, const void* residual, const float* gamma,
+                          float eps, void* residual_out, void* y, const qkn_fp8_rows* q, void* stream) {
+  if (!check_dtype(dtype) || !q || !(eps >= 0.f) || !isfinite(eps)) return QKN_ERR_INVALID_ARG;
+  if (q->ld_scale < 4 || !check_fp8(q->codes, q->scale, q->rows, q->cols, q->ld, q->ld_scale))
+    return QKN_ERR_INVALID_ARG;
+  if (ld_x < q->cols || (residual == nullptr) != (residual_out == nullptr)) return QKN_ERR_INVALID_ARG;
+  if (q->rows == 0) return QKN_OK;
+  const size_t e = elem_size(dtype);
+  if (!x || !aligned(x, e) || !aligned(residual, e) || !aligned(residual_out, e) || !aligned(y, e) ||
+      !aligned(gamma, 4))
+    return QKN_ERR_INVALID_ARG;
+  // in place only where every row lies over itself, and not where a later read needs what was there
+  if ((residual_out == x || y == x) && ld_x != q->cols) return QKN_ERR_INVALID_ARG;
+  if (y && (y == residual || y == residual_out || (residual && y == x))) return QKN_ERR_INVALID_ARG;
+  NormQuantArgs a;
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.residual_out = residual_out;
+  a.y = y;
+  a.codes = static_cast<uint8_t*>(q->codes);
+  a.scale = q->scale;
+  a.ld_x = ld_x;
+  a.ld = q->ld;
+  a.ld_scale = q->ld_scale;
+  a.n = q->rows;
+  a.d = q->cols;
+  a.eps = eps;
+  cudaError_t err = launch_norm_quant(a, dtype == QKN_BF16, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? QKN_OK : QKN_ERR_CUDA;
+}
+
+qkn_status qkn_quant_weight(qkn_dtype dtype, const void* w, const qkn_fp8_weight* q, void* stream) {
+  if (!check_dtype(dtype) || !q || !check_fp8(q->codes, q->scale, q->rows, q->cols, q->ld, 0))
+    return QKN_ERR_INVALID_ARG;
+  if (q->rows == 0) return QKN_OK;
+  if (!w || !aligned(w, elem_size(dtype))) return QKN_ERR_INVALID_ARG;
+  QuantWeightArgs a;
+  a.w = w;
+  a.codes = static_cast<uint8_t*>(q->codes);
+  a.scale = q->scale;
+  a.ld = q->ld;
+  a.n = q->rows;
+  a.k = q->cols;
+  cudaError_t err = launch_quant_weight(a, dtype == QKN_BF16, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? QKN_OK : QKN_ERR_CUDA;
+}
+
+qkn_status qkn_fp8_linear(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dtype out_dtype, int32_t n_outs,
+                          const qkn_out_cols* outs, void* workspace, size_t ws_bytes, void* stream) {
+  if (!check_dtype(out_dtype) || !a || !w || !outs || n_outs < 1 || n_outs > QKN_MAX_OUTS) return QKN_ERR_INVALID_ARG;
+  if (a->ld_scale < 4 || !check_fp8(a->codes, a->scale, a->rows, a->cols, a->ld, a->ld_scale) ||
+      !check_fp8(w->codes, w->scale, w->rows, w->cols, w->ld, 0))
+    return QKN_ERR_INVALID_ARG;
+  if (w->rows < 1 || a->cols != w->cols) return QKN_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < (size_t)kStatusBytes) return QKN_ERR_INVALID_ARG;
+  Fp8LinearArgs l;
+  int64_t at = 0;
+  for (int i = 0; i < n_outs; ++i) {
+    if (outs[i].cols < 1 || outs[i].ld < outs[i].cols || at + outs[i].cols > w->rows) return QKN_ERR_INVALID_ARG;
+    if (a->rows > 0 && (!outs[i].out || !aligned(outs[i].out, elem_size(out_dtype)))) return QKN_ERR_INVALID_ARG;
+    l.outs[i] = OutCols{outs[i].out, (int32_t)at, (int32_t)(at + outs[i].cols), outs[i].ld};
+    at += outs[i].cols;
+  }
+  if (at != w->rows) return QKN_ERR_INVALID_ARG;
+  if (a->rows == 0) return QKN_OK;
+  l.a = static_cast<const uint8_t*>(a->codes);
+  l.a_scale = a->scale;
+  l.w = static_cast<const uint8_t*>(w->codes);
+  l.w_scale = w->scale;
+  l.lda = a->ld;
+  l.ld_as = a->ld_scale;
+  l.ldw = w->ld;
+  l.m = a->rows;
+  l.n = w->rows;
+  l.k = a->cols;
+  l.n_outs = n_outs;
+  l.status = static_cast<int32_t*>(workspace);
+  cudaError_t err = launch_fp8_linear(l, out_dtype == QKN_BF16, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? QKN_OK : QKN_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -167,6 +167,56 @@ cudaError_t launch_gqa_decode(const GqaDecodeArgs& a, cudaStream_t st);
 // The merge of the GQA route's split partials (combine.cu, grouped row tiles).
 cudaError_t launch_combine_grouped(const CombineArgs& a, cudaStream_t st);
 
+// The 8-bit projections (quant.cu, fp8_linear.cu).  A scale covers kFp8Group columns (and, in a
+// weight, as many rows); it is the block's largest magnitude over kFp8Top, the largest e4m3 value,
+// and at least kFp8Least, so that an all-zero block has a reciprocal.
+constexpr int kFp8Group = 128;
+constexpr float kFp8Top = 448.f;
+constexpr float kFp8Least = 7.888609052210118e-31f;   // 2^-100
+
+struct NormQuantArgs {
+  const void* x;           // [n, ld_x]
+  const void* residual;    // [n, d] or null
+  const float* gamma;      // [d] or null (no norm)
+  void* residual_out;      // [n, d], with residual
+  void* y;                 // [n, d] or null
+  uint8_t* codes;          // [n, ld]
+  float* scale;            // [ceil(d / 128), ld_scale]
+  int64_t ld_x, ld, ld_scale;
+  int32_t n, d;
+  float eps;
+};
+
+struct QuantWeightArgs {
+  const void* w;           // [n, k]
+  uint8_t* codes;          // [n, ld]
+  float* scale;            // [ceil(n / 128), ceil(k / 128)]
+  int64_t ld;
+  int32_t n, k;
+};
+
+struct OutCols {
+  void* out;
+  int32_t begin, end;      // columns [begin, end) of the product
+  int64_t ld;
+};
+
+struct Fp8LinearArgs {
+  const uint8_t* a;        // [m, lda]
+  const float* a_scale;    // [ceil(k / 128), ld_as]
+  const uint8_t* w;        // [n, ldw]
+  const float* w_scale;    // [ceil(n / 128), ceil(k / 128)]
+  int64_t lda, ld_as, ldw;
+  int32_t m, n, k;
+  int32_t n_outs;
+  OutCols outs[QKN_MAX_OUTS];
+  int32_t* status;         // workspace status word
+};
+
+cudaError_t launch_norm_quant(const NormQuantArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_quant_weight(const QuantWeightArgs& a, bool bf16, cudaStream_t st);
+cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, bool bf16_out, cudaStream_t st);
+
 cudaError_t launch_append(const AppendArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_key_gram(const float* w_k, float* gram, int groups, int r, int width, cudaStream_t st);
 // One launch for both (prep.cu) when the append can run as one launch and is a decode step's size.

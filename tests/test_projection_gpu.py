@@ -1,0 +1,296 @@
+"""The 8-bit projections on the GPU against their definitions in 64 bits.
+
+Tolerances, from the roundings alone (u = 2^-24, half a step of fp32):
+  * h: the fp32 sum and its rounding to the storage type: |h64| (2^-8 + u) in bf16, |h64| u in fp32;
+  * scale: a sum of d squares in a tree of at most d / 256 + 32 additions in a row (half of its relative
+    error after the square root), the root, the divisions and the products: (d / 256 + 40) u;
+  * a code: half a step of e4m3 (2^-4 of the value, 2^-10 below the normal range) around y / scale, whose
+    own error is at most the scale's and the reciprocal's (another d / 256 + 48 units);
+  * a product: every addition within a block may lose up to one unit of fp32 (2 u) of the block's sum of
+    magnitudes, every block's entry into the total u: (2 * 128 + blocks + 4) u sum|a||w|, and half a step
+    of bf16 (2^-8) of the result.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import qk_normed_latent_qkn_b200 as qkn
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: U}
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+def hidden(n, d, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn((n, d), generator=g) * torch.exp(0.5 * torch.randn((n, 1), generator=g))
+    return (x * torch.where(torch.rand((1, d), generator=g) < 1 / 64, 12.0, 1.0)).to(dtype).cuda()
+
+
+def check_codes(codes, scale, y, d_chain):
+    """codes [n, d] and scale [g, n] on the host against y [n, d] in 64 bits."""
+    ratio, want = oracle.quant_rows(y)
+    tol = (d_chain // 256 + 40) * U
+    assert np.abs(scale / want - 1).max() <= tol
+    slack = (2 * tol + 8 * U) * np.abs(ratio)
+    assert np.all(np.abs(codes - ratio) <= np.maximum(np.abs(ratio) * 2.0 ** -4, 2.0 ** -10) + slack)
+
+
+def run_norm(x, gamma=None, residual=None, want_y=False, eps=1e-6, inplace=False):
+    n, d = x.shape
+    q = qkn.Fp8Rows.empty(n, d)
+    q.codes.view(torch.uint8).fill_(0x35)
+    q.scale.fill_(-7.0)
+    h = None if residual is None else (residual if inplace else torch.empty_like(residual))
+    y = torch.empty((n, d), dtype=x.dtype, device="cuda") if want_y else None
+    qkn.norm_quant(x, q, gamma=gamma, eps=eps, residual=residual, residual_out=h, y=y)
+    torch.cuda.synchronize()
+    # nothing behind a row's codes or a block's scales is written
+    assert (q.codes.view(torch.uint8)[:, d:] == 0x35).all() and (q.scale[:, n:] == -7.0).all()
+    return q, h, y
+
+
+SHAPES = [(1, 1), (1, 2048), (3, 64), (2, 127), (5, 128), (4, 129), (7, 136), (33, 4096), (9, 5000), (130, 1000),
+          (2, 16384), (3, 32768), (2, 32776), (2, 40001), (257, 576)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", SHAPES)
+@pytest.mark.parametrize("form", ["norm", "residual", "plain", "sum"])
+def test_norm_quant(n, d, dtype, form):
+    x = hidden(n, d, dtype, seed=n * 7 + d)
+    res = hidden(n, d, dtype, seed=n + d * 3 + 1) * 2 if form in ("residual", "sum") else None
+    gamma = (1 + 0.1 * torch.randn(d, generator=torch.Generator().manual_seed(d))).cuda() if form in (
+        "norm", "residual") else None
+    q, h, y = run_norm(x, gamma, res, want_y=gamma is not None)
+    h64 = host(x)
+    if res is not None:
+        total = host(x) + host(res)
+        h64 = host(h)
+        assert np.all(np.abs(h64 - total) <= np.abs(total) * (HALF_STEP[dtype] + U) + 1e-40)
+    y64 = h64 if gamma is None else oracle.rms_norm(h64, host(gamma), 1e-6)
+    check_codes(host(q.codes[:, :d]), host(q.scale[:, :n]), y64, d if gamma is not None else 0)
+    if y is not None:
+        assert np.all(np.abs(host(y) - y64) <= np.abs(y64) * (HALF_STEP[dtype] + (d // 256 + 40) * U))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("d", [512, 500, 40001])
+def test_norm_quant_in_place_and_strided_rows(dtype, d):
+    """The sum may be written over the residual or over x, and x may be a slice of wider rows; unaligned rows
+    take the same values."""
+    n = 6
+    x, res = hidden(n, d, dtype, 1), hidden(n, d, dtype, 2)
+    gamma = torch.ones(d, device="cuda")
+    ref, h, _ = run_norm(x, gamma, res.clone())
+    q, h2, _ = run_norm(x, gamma, res.clone(), inplace=True)
+    assert torch.equal(h, h2) and torch.equal(ref.codes.view(torch.uint8)[:, :d], q.codes.view(torch.uint8)[:, :d])
+    xx = x.clone()
+    q = qkn.Fp8Rows.empty(n, d)
+    qkn.norm_quant(xx, q, gamma=gamma, residual=res, residual_out=xx)
+    assert torch.equal(xx, h) and torch.equal(ref.scale[:, :n], q.scale[:, :n])
+    xx = x.clone()
+    q1, q2 = qkn.Fp8Rows.empty(n, d), qkn.Fp8Rows.empty(n, d)
+    qkn.norm_quant(x, q1, gamma=gamma)
+    qkn.norm_quant(xx, q2, gamma=gamma, y=xx)
+    assert torch.equal(q1.scale[:, :n], q2.scale[:, :n])
+    assert torch.equal(q1.codes.view(torch.uint8)[:, :d], q2.codes.view(torch.uint8)[:, :d])
+    for off in (1, 8):          # a slice of wider rows, off the 16-byte grid and on it
+        wide = torch.full((n, d + 24), 9.0, dtype=dtype, device="cuda")
+        wide[:, off:off + d] = x
+        q3, _, _ = run_norm(wide[:, off:off + d], gamma)
+        y64 = oracle.rms_norm(host(x), host(gamma), 1e-6)
+        check_codes(host(q3.codes[:, :d]), host(q3.scale[:, :n]), y64, d)
+
+
+@pytest.mark.parametrize("d", [256, 250])
+def test_norm_quant_of_zeros_infinities_and_nan(d):
+    """A zero row has zero codes and the least scale; a NaN or an infinity spoils its block (with gamma, its row)
+    and no other row."""
+    x = hidden(5, d, torch.float32, 5)
+    x[1] = 0
+    x[2, 3] = float("nan")
+    x[3, 200] = float("inf")
+    x[4] = 1e-36
+    q, _, _ = run_norm(x)
+    v = oracle.row_values(host(q.codes[:, :d]), host(q.scale[:, :5]))
+    assert (v[1] == 0).all() and (host(q.scale)[:, 1] == 2.0 ** -100).all()
+    assert np.isnan(v[2, :128]).all() and np.isfinite(v[2, 128:]).all()
+    assert np.isnan(v[3, 128:]).all() and np.isfinite(v[3, :128]).all()
+    ratio, _ = oracle.quant_rows(host(x[4:]))
+    assert np.abs(host(q.codes)[4, :d] - oracle.e4m3_round(ratio)[0]).max() == 0
+    assert np.isfinite(v[0]).all()
+    q, _, _ = run_norm(x, torch.ones(d, device="cuda"))
+    v = oracle.row_values(host(q.codes[:, :d]), host(q.scale[:, :5]))
+    assert (v[1] == 0).all() and np.isnan(v[2]).all() and np.isnan(v[3, 128:]).all()
+    assert np.isfinite(v[[0, 4]]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,k", [(1, 1), (64, 512), (128, 128), (129, 130), (576, 2048), (200, 1000), (300, 77), (7, 4104)])
+def test_quant_weight(n, k, dtype):
+    w = (torch.randn((n, k), generator=torch.Generator().manual_seed(n + k)) / k ** 0.5).to(dtype).cuda()
+    q = qkn.Fp8Weight.empty(n, k)
+    q.codes.view(torch.uint8).fill_(0x35)
+    qkn.quant_weight(w, q)
+    ratio, want = oracle.quant_weight(host(w))
+    assert np.abs(host(q.scale) / want - 1).max() <= 2 * U
+    slack = 8 * U * np.abs(ratio)
+    assert np.all(np.abs(host(q.codes[:, :k]) - ratio) <= np.maximum(np.abs(ratio) * 2.0 ** -4, 2.0 ** -10) + slack)
+    assert (q.codes.view(torch.uint8)[:, k:] == 0x35).all()
+
+
+def test_quant_weight_keeps_nan_in_its_block():
+    w = torch.randn((256, 256), device="cuda")
+    w[130, 5] = float("nan")
+    w[3, 250] = float("inf")
+    q = qkn.Fp8Weight.empty(256, 256)
+    qkn.quant_weight(w, q)
+    v = oracle.weight_values(host(q.codes), host(q.scale))
+    assert np.isnan(v[128:, :128]).all() and np.isnan(v[:128, 128:]).all()
+    assert np.isfinite(v[:128, :128]).all() and np.isfinite(v[128:, 128:]).all()
+
+
+# ---------------------------------------------------------------- the product
+def operands(m, n, k, seed=0, pad=0):
+    """Codes and scales of rows and a weight; what lies behind the edges is poisoned with NaN codes."""
+    x = hidden(m, k, torch.float32, seed)
+    a = qkn.Fp8Rows.empty(m, k)
+    if pad:
+        a = qkn.Fp8Rows(torch.empty((m, a.codes.shape[1] + pad), dtype=torch.float8_e4m3fn, device="cuda"), a.scale, k)
+    a.codes.view(torch.uint8).fill_(0x7F)
+    a.scale.fill_(float("nan"))
+    qkn.norm_quant(x, a)
+    w32 = (torch.randn((n, k), generator=torch.Generator().manual_seed(seed + 1)) / k ** 0.5).cuda()
+    w = qkn.Fp8Weight.empty(n, k)
+    w.codes.view(torch.uint8).fill_(0x7F)
+    qkn.quant_weight(w32, w)
+    return a, w
+
+
+def product(a, w):
+    m, n, k = a.rows, w.rows, a.cols
+    av = oracle.row_values(host(a.codes[:, :k]), host(a.scale[:, :m]))
+    wv = oracle.weight_values(host(w.codes[:, :k]), host(w.scale))
+    return av @ wv.T, np.abs(av) @ np.abs(wv).T
+
+
+def check_product(out, ref, mag, k, dtype):
+    tol = (2 * 128 + (k + 127) // 128 + 4) * U * mag
+    if dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * np.abs(ref)
+    err = np.abs(out - ref)
+    assert np.isfinite(out).all()
+    assert np.all(err <= tol), f"worst {np.max(err / np.maximum(tol, 1e-300)):.3f} of the tolerance"
+
+
+def workspace():
+    ws = torch.empty(qkn.WORKSPACE_BYTES, dtype=torch.uint8, device="cuda")
+    qkn.workspace_init(ws)
+    return ws
+
+
+LINEAR = [  # m, n, k, widths
+    (1, 1, 1, [1]), (1, 576, 2048, [512, 64]), (2, 64, 128, [64]), (16, 130, 256, [130]), (17, 128, 384, [1, 127]),
+    (5, 7, 77, [3, 4]), (31, 1000, 1960, [904, 96]), (33, 257, 144, [257]), (64, 640, 4096, [512, 64, 64]),
+    (65, 384, 1000, [384]), (100, 2000, 130, [1000, 1000]), (128, 512, 512, [512]), (129, 264, 640, [8, 256]),
+    (200, 1029, 900, [5, 1024]), (256, 256, 128, [256]), (300, 700, 3000, [700]), (333, 1000, 1960, [904, 96]),
+    (513, 1536, 512, [1024, 8, 504]), (1000, 3333, 260, [1111, 1111, 1111]), (2049, 520, 256, [520]),
+    (4, 4096, 16384, [4096]), (48, 12288, 512, [8192, 4096]), (1, 25152, 640, [16384, 8192, 512, 64]),
+    (700, 2560, 128, [320] * 8),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n,k,widths", LINEAR)
+def test_fp8_linear(m, n, k, widths, dtype):
+    a, w = operands(m, n, k, seed=m + n + k)
+    outs = [torch.full((m, c), float("nan"), dtype=dtype, device="cuda") for c in widths]
+    ws = workspace()
+    qkn.fp8_linear(a, w, outs, ws)
+    torch.cuda.synchronize()
+    assert qkn.read_device_status(ws) == qkn.OK
+    ref, mag = product(a, w)
+    check_product(np.concatenate([host(o) for o in outs], axis=1), ref, mag, k, dtype)
+
+
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_fp8_linear_strides_and_alignment(m):
+    """Outputs as slices of wider buffers at odd places, codes with a longer row: what lies around stays."""
+    n, k = 520, 400
+    a, w = operands(m, n, k, seed=9, pad=48)
+    ref, mag = product(a, w)
+    for dtype in DTYPES:
+        for off, widths in ((0, [520]), (1, [260, 260]), (3, [8, 509, 3]), (8, [512, 8])):
+            bufs = [torch.full((m, c + 16), 5.0, dtype=dtype, device="cuda") for c in widths]
+            qkn.fp8_linear(a, w, [b[:, off:off + c] for b, c in zip(bufs, widths)], workspace())
+            got = np.concatenate([host(b[:, off:off + c]) for b, c in zip(bufs, widths)], axis=1)
+            check_product(got, ref, mag, k, dtype)
+            for b, c in zip(bufs, widths):
+                assert (b[:, :off] == 5.0).all() and (b[:, off + c:] == 5.0).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 700, 4096), (300, 520, 640), (700, 2560, 384)])
+def test_fp8_linear_repeats_bit_for_bit_and_keeps_nan_in_its_row(m, n, k):
+    a, w = operands(m, n, k, seed=2)
+    a.scale[1, 1] = float("nan")
+    outs = [torch.empty((m, n), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    ws = workspace()
+    for o in outs:
+        qkn.fp8_linear(a, w, [o], ws)
+    bits = [o.view(torch.int16) for o in outs]
+    assert torch.equal(bits[0], bits[1]) and torch.equal(bits[0], bits[2])
+    assert torch.isnan(outs[0][1]).all() and torch.isfinite(outs[0][0]).all() and torch.isfinite(outs[0][2:]).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 576, 2048), (32, 2000, 1024), (333, 1000, 1960), (1024, 2560, 512)])
+def test_norm_and_product_captured_replayed_and_on_two_streams(m, n, k):
+    """The pair in a CUDA graph over fixed buffers, replayed on new inputs, and two at once on two streams that
+    share a workspace: the same bits as one after the other."""
+    gamma = torch.ones(k, device="cuda")
+    w = operands(1, n, k, seed=3)[1]
+    ws = workspace()
+
+    def buffers():
+        return (hidden(m, k, torch.bfloat16, 0), qkn.Fp8Rows.empty(m, k),
+                torch.empty((m, n), dtype=torch.bfloat16, device="cuda"))
+
+    def run(b):
+        qkn.norm_quant(b[0], b[1], gamma=gamma)
+        qkn.fp8_linear(b[1], w, [b[2]], ws)
+
+    xs = [hidden(m, k, torch.bfloat16, s) for s in range(3)]
+    want = []
+    b = buffers()
+    for x in xs:
+        b[0].copy_(x)
+        run(b)
+        want.append(b[2].clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(b)
+    for x, o in zip(xs, want):
+        b[0].copy_(x)
+        b[2].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(b[2], o)
+    pairs = [(torch.cuda.Stream(), buffers()) for _ in range(3)]
+    for (st, p), x in zip(pairs, xs):
+        p[0].copy_(x)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for st, p in pairs:
+            with torch.cuda.stream(st):
+                run(p)
+    torch.cuda.synchronize()
+    for (st, p), o in zip(pairs, want):
+        assert torch.equal(p[2], o)
+    assert qkn.read_device_status(ws) == qkn.OK
