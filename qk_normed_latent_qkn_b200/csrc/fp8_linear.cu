@@ -1,70 +1,557 @@
 // qkn_fp8_linear: out = A W^T for rows and a weight in 8 bits with a scale for each block of 128.
 //
-// out[i, n] = sum_b sa[b, i] sw[n / 128, b] sum_{k in b} a[i, k] w[n, k].  The products of two e4m3
-// values are exact in fp32, a block's 128 of them are summed unscaled, and each block's sum enters
-// the fp32 total with its two scales; one rounding at the end.
-#include <cuda_fp8.h>
+// Mathematics.  out[i, n] = sum_b sa[b, i] sw[n / 128, b] sum_{k in b} a[i, k] w[n, k].  The products
+// of two e4m3 values are exact in fp32; the tensor core sums the 128 of a block into a fresh TMEM
+// accumulator, and the epilogue warps enter it into the fp32 total that they keep in registers, with
+// the block's two scales.  One rounding, at the end.
+//
+// Two kernels, both fed by TMA (128-byte swizzled boxes of 128 codes, which zero-fill whatever lies
+// behind the last row or column, so no size needs to be a multiple of anything):
+//   * linear_pair_kernel, many rows: pairs of CTAs share a tile of 256 rows x 256 columns
+//     (cta_group::2), persistent over the tiles;
+//   * linear_split_kernel, few rows: the weight's 128 columns take the tensor core's M, the rows its N
+//     (16 to 128), and a cluster of up to 8 CTAs splits K and joins through distributed shared memory.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace qkn {
+
+using namespace sm100;
+
+struct LinearMaps {
+  CUtensorMap a, w, a_scale;
+};
+
 namespace {
 
-constexpr int kTile = 64;
+constexpr int64_t kWaitCycles = 2000000000LL;   // about a second: any wait that long is a fault
+constexpr int kRowBytes = 128;                  // codes of one block of K in a tile row
+constexpr int kTileBytes = 128 * kRowBytes;     // 128 rows of a tile
+constexpr int kKStep = 32;                      // K of one MMA
+constexpr uint32_t kDescStep = kKStep >> 4;     // the same in descriptor units
 
-__device__ __forceinline__ float value_of(uint8_t code) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
+template <typename O>
+__device__ __forceinline__ bool wide_ok(const OutCols& o) {
+  constexpr int E = 16 / (int)sizeof(O);
+  return (reinterpret_cast<uintptr_t>(o.out) & 15) == 0 && o.ld % E == 0 && o.begin % E == 0;
 }
 
-// A tile of 64 x 64 outputs per CTA, 4 x 4 per thread, on the CUDA cores.
+// N (a multiple of 8) consecutive columns of one row, from column col of the product.
+template <typename O, int N>
+__device__ __forceinline__ void store_cols(const Fp8LinearArgs& p, int64_t row, int col, const float (&v)[N]) {
+  if (col >= p.n) return;
+  int o = 0;
+  while (col >= p.outs[o].end) ++o;
+  if (col + N <= p.outs[o].end && wide_ok<O>(p.outs[o])) {
+    O* dst = static_cast<O*>(p.outs[o].out) + row * p.outs[o].ld + (col - p.outs[o].begin);
+    if constexpr (sizeof(O) == 4) {
+#pragma unroll
+      for (int e = 0; e < N; e += 4)
+        *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 8) {
+        uint4 u;
+        __nv_bfloat162 t[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(v[e + 2 * i], v[e + 2 * i + 1]);
+        u.x = *reinterpret_cast<uint32_t*>(&t[0]);
+        u.y = *reinterpret_cast<uint32_t*>(&t[1]);
+        u.z = *reinterpret_cast<uint32_t*>(&t[2]);
+        u.w = *reinterpret_cast<uint32_t*>(&t[3]);
+        *reinterpret_cast<uint4*>(dst + e) = u;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (col + e >= p.n) return;
+    while (col + e >= p.outs[o].end) ++o;
+    static_cast<O*>(p.outs[o].out)[row * p.outs[o].ld + (col + e - p.outs[o].begin)] = from_f32<O>(v[e]);
+  }
+}
+
+// Packed pairs of fp32 (the sm_100 FMA takes two at a time).
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+
+// ---------------------------------------------------------------- many rows: CTA pairs
+constexpr int kPairM = 256, kPairN = 256;       // tile of a pair
+constexpr int kPairStages = 6;
+constexpr int kPairStageBytes = 2 * kTileBytes; // this CTA's 128 rows of A and 128 of W
+constexpr int kPairThreads = 320;               // producer, MMA, 8 epilogue warps
+constexpr int kPairGroupM = 16;                 // row tiles that are walked before the next column tile
+
+struct PairBars {
+  uint64_t full[kPairStages], empty[kPairStages];
+  uint64_t t_full[2], t_empty[2];
+  uint32_t tmem;
+};
+constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 1024;
+
+struct TileWalk {
+  int mt, nt;
+  __device__ __forceinline__ void of(int64_t t, int& m, int& n) const {
+    const int64_t per = (int64_t)kPairGroupM * nt;
+    const int g = (int)(t / per);
+    const int rows = min(kPairGroupM, mt - g * kPairGroupM);
+    const int r = (int)(t - (int64_t)g * per);
+    m = g * kPairGroupM + r % rows;
+    n = r / rows;
+  }
+};
+
+// Warps: 0 producer, 1 MMA (the even CTA issues for both), 2-9 epilogue (each CTA its 128 rows; warps
+// 2-5 the tile's first 128 columns, 6-9 the others).
 template <typename O>
-__global__ void __launch_bounds__(256) fp8_linear_simple_kernel(Fp8LinearArgs p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ Fp8LinearArgs p, const __grid_constant__ LinearMaps maps) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairStages * kPairStageBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t stages = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kPairStages; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 1);
+      mbar_init(smem_u32(&bars.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&bars.t_full[i]), 1);
+      mbar_init(smem_u32(&bars.t_empty[i]), 16);   // 8 epilogue warps of each CTA
+    }
+    mbar_fence_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.w);
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&bars.tmem), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
   pdl_trigger();
   pdl_wait();
-  __shared__ float sa[32][kTile + 1], sw[32][kTile + 1];
-  const int i0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int groups = (p.k + kFp8Group - 1) / kFp8Group;
-  float acc[4][4] = {};
-  for (int b = 0; b < groups; ++b) {
-    float t[4][4] = {};
-    for (int k0 = b * kFp8Group; k0 < min(p.k, (b + 1) * kFp8Group); k0 += 32) {
-      for (int e = threadIdx.x; e < kTile * 32; e += 256) {
-        const int row = e / 32, k = e % 32;
-        const bool in = k0 + k < p.k;
-        sa[k][row] = in && i0 + row < p.m ? value_of(p.a[(int64_t)(i0 + row) * p.lda + k0 + k]) : 0.f;
-        sw[k][row] = in && n0 + row < p.n ? value_of(p.w[(int64_t)(n0 + row) * p.ldw + k0 + k]) : 0.f;
+
+  const TileWalk walk{(p.m + kPairM - 1) / kPairM, (p.n + kPairN - 1) / kPairN};
+  const int64_t tiles = (int64_t)walk.mt * walk.nt;
+  const int blocks = (p.k + kFp8Group - 1) / kFp8Group;
+  const int pairs = gridDim.x >> 1;
+  bool ok = true;
+
+  if (warp == 0) {
+    RingPos<kPairStages> ring;
+    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+      int m, n;
+      walk.of(t, m, n);
+      const int y_a = m * kPairM + (int)rank * 128, y_w = n * kPairN + (int)rank * 128;
+      for (int b = 0; b < blocks; ++b) {
+        if (!mbar_wait_warp_cl(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
+        const uint32_t full = smem_u32(&bars.full[ring.slot]);
+        if (rank == 0) mbar_arrive_expect_tx_elect(full, 2 * kPairStageBytes);
+        const uint32_t dst = stages + ring.slot * kPairStageBytes;
+        const uint32_t bar = mapa_shared(full, 0);
+        tma_load_2d_pair_elect(dst, &maps.a, b * kFp8Group, y_a, bar);
+        tma_load_2d_pair_elect(dst + kTileBytes, &maps.w, b * kFp8Group, y_w, bar);
+        ring.next();
       }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) t[i][j] += sa[k][ty * 4 + i] * sw[k][tx * 4 + j];
-      __syncthreads();
     }
-    const float s = p.w_scale[(int64_t)(n0 / kFp8Group) * groups + b];
-    for (int i = 0; i < 4; ++i) {
-      const int row = i0 + ty * 4 + i;
-      const float u = row < p.m ? p.a_scale[b * p.ld_as + row] * s : 0.f;
-      for (int j = 0; j < 4; ++j) acc[i][j] += t[i][j] * u;
+    // the last uses of the stages end before this CTA does: their commits arrive here
+    for (int i = 0; i < kPairStages; ++i) {
+      if (!mbar_wait_warp_cl(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
+      ring.next();
+    }
+  } else if (warp == 1 && rank == 0) {
+    constexpr uint32_t idesc = idesc_e4m3(256, 256);
+    const uint64_t d_a = smem_desc(stages, 16, 1024), d_w = smem_desc(stages + kTileBytes, 16, 1024);
+    RingPos<kPairStages> ring;
+    RingPos<2> acc;
+    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs)
+      for (int b = 0; b < blocks; ++b) {
+        if (!mbar_wait_warp_cl(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles) ||
+            !mbar_wait_warp_cl(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t at = (uint64_t)((ring.slot * kPairStageBytes) >> 4);
+#pragma unroll
+        for (int s = 0; s < kFp8Group / kKStep; ++s)
+          mma_e4m3_pair_elect(tmem + acc.slot * kPairN, d_a + at + s * kDescStep, d_w + at + s * kDescStep, idesc,
+                              s > 0);
+        mma_commit_group2_elect(smem_u32(&bars.empty[ring.slot]), 3);
+        mma_commit_group2_elect(smem_u32(&bars.t_full[acc.slot]), 3);
+        ring.next();
+        acc.next();
+      }
+  } else if (warp >= 2) {
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    RingPos<2> acc;
+    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+      int m, n;
+      walk.of(t, m, n);
+      const int row = m * kPairM + (int)rank * 128 + quad * 32 + lane;
+      const int col = n * kPairN + half * 128;
+      const float* sa = p.a_scale + min(row, p.m - 1);
+      const float* sw = p.w_scale + (int64_t)min(col / kFp8Group, (p.n - 1) / kFp8Group) * blocks;
+      uint64_t total[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) total[i] = 0;
+      // the next block's scales are on their way while this one's sums are entered
+      float s_next = __ldg(sa) * __ldg(sw);
+      for (int b = 0; b < blocks; ++b) {
+        const float s = s_next;
+        const int bn = min(b + 1, blocks - 1);
+        const float sa_n = __ldg(sa + bn * p.ld_as), sw_n = __ldg(sw + bn);
+        if (!mbar_wait_warp_cl(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc.slot * kPairN + half * 128;
+        const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+        uint32_t v[2][16];
+        tmem_ld16(at, v[0]);
+        tmem_wait_ld(v[0]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (c < 7) tmem_ld16(at + (c + 1) * 16, v[(c + 1) & 1]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) fma2(total[c * 8 + e], pack2(v[c & 1][2 * e], v[c & 1][2 * e + 1]), s2);
+          if (c < 7) tmem_wait_ld(v[(c + 1) & 1]);
+          if (c == 6) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote_release(mapa_shared(smem_u32(&bars.t_empty[acc.slot]), 0));
+          }
+        }
+        acc.next();
+        s_next = sa_n * sw_n;
+      }
+      if (ok && row < p.m) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) unpack2(total[c * 8 + e], v[2 * e], v[2 * e + 1]);
+          store_cols<O>(p, row, col + c * 16, v);
+        }
+      }
     }
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int row = i0 + ty * 4 + i, col = n0 + tx * 4 + j;
-      if (row >= p.m || col >= p.n) continue;
-      int o = 0;
-      while (col >= p.outs[o].end) ++o;
-      static_cast<O*>(p.outs[o].out)[row * p.outs[o].ld + col - p.outs[o].begin] = from_f32<O>(acc[i][j]);
+  __syncwarp();
+  if (!ok && lane == 0) record_status(p.status, QKN_ERR_TIMEOUT);
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- few rows: K split over a cluster
+template <int NT>
+struct SplitCfg {
+  static constexpr int kStageBytes = kTileBytes + NT * kRowBytes + 1024;  // weight, rows, the rows' scales
+  static constexpr int kStages = NT == 128 ? 3 : NT == 64 ? 4 : 5;
+  static constexpr int kCols = NT < 32 ? 32 : NT;                        // TMEM columns of one accumulator
+  static constexpr int kAccs = NT == 128 ? 2 : 4;
+  static constexpr int kBarOff = kStages * kStageBytes;
+  static constexpr int kSmem = 1024 + kBarOff + 256;
+  static constexpr int kThreads = 192;                                    // producer, MMA, 4 epilogue warps
+  static_assert(NT * 128 * 4 <= kBarOff, "the partial sums reuse the stages");
+  static_assert(kTileBytes % 1024 == 0 && (NT * kRowBytes) % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+
+template <int S, int A>
+struct SplitBars {
+  uint64_t full[S], empty[S];
+  uint64_t t_full[A], t_empty[A];
+  uint32_t tmem;
+};
+
+// One tile: 128 columns of the product for NT rows.  Cluster rank r takes the r-th part of K's blocks.
+// Warps: 0 producer, 1 MMA, 2-5 epilogue.
+template <int NT, typename O>
+__global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant__ Fp8LinearArgs p,
+                                                           const __grid_constant__ LinearMaps maps, int split,
+                                                           int row_tiles) {
+  using C = SplitCfg<NT>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+  auto& bars = *reinterpret_cast<SplitBars<C::kStages, C::kAccs>*>(smem + C::kBarOff);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % split;                     // (clusters lie along x)
+  const int tile = blockIdx.x / split;
+  const int row0 = (tile % row_tiles) * NT, n0 = (tile / row_tiles) * 128;
+  const int rows = min(NT, p.m - row0);
+  const int blocks = (p.k + kFp8Group - 1) / kFp8Group;
+  const int b0 = (int)((int64_t)blocks * rank / split), b1 = (int)((int64_t)blocks * (rank + 1) / split);
+  const uint32_t stages = smem_u32(smem);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(smem_u32(&bars.full[i]), 1);
+      mbar_init(smem_u32(&bars.empty[i]), 5);              // the MMA's commit and the 4 epilogue warps
     }
+    for (int i = 0; i < C::kAccs; ++i) {
+      mbar_init(smem_u32(&bars.t_full[i]), 1);
+      mbar_init(smem_u32(&bars.t_empty[i]), 4);
+    }
+    mbar_fence_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.w);
+    prefetch_tmap(&maps.a_scale);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&bars.tmem), C::kCols * C::kAccs);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  pdl_trigger();
+  pdl_wait();
+
+  bool ok = true;
+  float total[NT];
+  if (warp == 0) {
+    RingPos<C::kStages> ring;
+    for (int b = b0; b < b1; ++b) {
+      if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
+      const uint32_t full = smem_u32(&bars.full[ring.slot]);
+      const uint32_t dst = stages + ring.slot * C::kStageBytes;
+      mbar_arrive_expect_tx_elect(full, kTileBytes + NT * kRowBytes + NT * 4);
+      tma_load_2d_elect(dst, &maps.w, b * kFp8Group, n0, full);
+      tma_load_2d_elect(dst + kTileBytes, &maps.a, b * kFp8Group, row0, full);
+      tma_load_2d_elect(dst + kTileBytes + NT * kRowBytes, &maps.a_scale, row0, b, full);
+      ring.next();
+    }
+    for (int i = 0; i < C::kStages; ++i) {                  // nothing of this CTA's is in flight after this
+      if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
+      ring.next();
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_e4m3(128, NT);
+    const uint64_t d_w = smem_desc(stages, 16, 1024), d_a = smem_desc(stages + kTileBytes, 16, 1024);
+    RingPos<C::kStages> ring;
+    RingPos<C::kAccs> acc;
+    for (int b = b0; b < b1; ++b) {
+      if (!mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles) ||
+          !mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint64_t at = (uint64_t)((ring.slot * C::kStageBytes) >> 4);
+#pragma unroll
+      for (int s = 0; s < kFp8Group / kKStep; ++s)
+        mma_e4m3_elect(tmem + acc.slot * C::kCols, d_w + at + s * kDescStep, d_a + at + s * kDescStep, idesc, s > 0);
+      mma_commit_elect(smem_u32(&bars.empty[ring.slot]));
+      mma_commit_elect(smem_u32(&bars.t_full[acc.slot]));
+      ring.next();
+      acc.next();
+    }
+  } else {
+    const int quad = warp & 3;
+    const float* sw = p.w_scale + (int64_t)(n0 / kFp8Group) * blocks;
+    RingPos<C::kStages> ring;
+    RingPos<C::kAccs> acc;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) total[i] = 0.f;
+    float sw_next = b0 < b1 ? __ldg(sw + b0) : 0.f;
+    for (int b = b0; b < b1; ++b) {
+      const float s = sw_next;
+      sw_next = __ldg(sw + min(b + 1, b1 - 1));
+      // the rows' scales are ordinary reads of what the copy wrote: wait for its barrier too
+      if (!mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles) ||
+          !mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const float4* sa = reinterpret_cast<const float4*>(smem + ring.slot * C::kStageBytes + kTileBytes + NT * kRowBytes);
+      const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc.slot * C::kCols;
+#pragma unroll
+      for (int c = 0; c < NT; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(at + c, v);
+        tmem_wait_ld(v);
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 f = sa[(c + e) >> 2];
+          total[c + e] += __uint_as_float(v[e]) * (f.x * s);
+          total[c + e + 1] += __uint_as_float(v[e + 1]) * (f.y * s);
+          total[c + e + 2] += __uint_as_float(v[e + 2]) * (f.z * s);
+          total[c + e + 3] += __uint_as_float(v[e + 3]) * (f.w * s);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars.t_empty[acc.slot]));
+        mbar_arrive(smem_u32(&bars.empty[ring.slot]));
+      }
+      ring.next();
+      acc.next();
+    }
+  }
+  __syncwarp();
+  if (!ok && lane == 0) record_status(p.status, QKN_ERR_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();                                          // every stage is free: the partial sums take their place
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kCols * C::kAccs);
+  }
+  float* part = reinterpret_cast<float*>(smem);             // [rows][128]
+  if (warp >= 2) {
+    const int c = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      if (j < rows) part[j * 128 + c] = total[j];
+  }
+  cluster_sync();
+  // rank r joins and writes the rows r, r + split, ... : 4 columns per lane, the parts in rank order
+  for (int j = rank + split * warp; j < rows; j += split * (C::kThreads / 32)) {
+    const uint32_t at = smem_u32(part + j * 128 + lane * 4);
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < split; ++r) {
+      const float4 f = ld_shared_remote_f4(mapa_shared(at, r));
+      v[0] += f.x;
+      v[1] += f.y;
+      v[2] += f.z;
+      v[3] += f.w;
+    }
+    const int col = n0 + lane * 4;
+    int o = 0;
+    for (int e = 0; e < 4 && col + e < p.n; ++e) {
+      while (col + e >= p.outs[o].end) ++o;
+      static_cast<O*>(p.outs[o].out)[(row0 + j) * p.outs[o].ld + (col + e - p.outs[o].begin)] = from_f32<O>(v[e]);
+    }
+  }
+  cluster_sync();                                           // no CTA leaves while its parts are read
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+bool make_map(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t rows,
+              uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_inner, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return fn(m, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Codes [rows, k] in boxes of 128 codes x box_rows rows.
+bool codes_map(CUtensorMap* m, const uint8_t* codes, int k, int rows, int64_t ld, int box_rows) {
+  return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, k, rows, ld, kRowBytes, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+template <typename O>
+cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
+  LinearMaps maps;
+  if (!codes_map(&maps.a, a.a, a.k, a.m, a.lda, 128) || !codes_map(&maps.w, a.w, a.k, a.n, a.ldw, 128))
+    return cudaErrorInvalidValue;
+  static PerDeviceOnce attrs;
+  cudaError_t e = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(linear_pair_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+  });
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)ceil_div(a.m, kPairM) * ceil_div(a.n, kPairN);
+  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+  return launch_chained(linear_pair_kernel<O>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, a, maps);
+}
+
+template <int NT, typename O>
+cudaError_t launch_split(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
+  using C = SplitCfg<NT>;
+  LinearMaps maps;
+  if (!codes_map(&maps.a, a.a, a.k, a.m, a.lda, NT) || !codes_map(&maps.w, a.w, a.k, a.n, a.ldw, 128) ||
+      !make_map(&maps.a_scale, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.a_scale, a.m, ceil_div(a.k, kFp8Group), a.ld_as * 4,
+                NT, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  static PerDeviceOnce attrs;
+  cudaError_t e = once_per_device(attrs, [] { return set_smem_attrs(linear_split_kernel<NT, O>, C::kSmem); });
+  if (e != cudaSuccess) return e;
+  const int row_tiles = ceil_div(a.m, NT), blocks = ceil_div(a.k, kFp8Group);
+  const int64_t tiles = (int64_t)row_tiles * ceil_div(a.n, 128);
+  // as many parts of K as fill the GPU with two CTAs on every SM, each with a block at least
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 2 * sms && split * 2 <= blocks) split *= 2;
+  if (tiles * split > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * split));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, O>, a, maps, split, row_tiles);
+}
+
+template <typename O>
+cudaError_t launch(const Fp8LinearArgs& a, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  if (a.m > 128) return launch_pair<O>(a, sms, st);
+  if (a.m > 64) return launch_split<128, O>(a, sms, st);
+  if (a.m > 32) return launch_split<64, O>(a, sms, st);
+  if (a.m > 16) return launch_split<32, O>(a, sms, st);
+  return launch_split<16, O>(a, sms, st);
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_linear(const Fp8LinearArgs& a, bool bf16_out, cudaStream_t st) {
-  const dim3 grid((a.n + kTile - 1) / kTile, (a.m + kTile - 1) / kTile);
-  return bf16_out ? launch_chained(fp8_linear_simple_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, a)
-                  : launch_chained(fp8_linear_simple_kernel<float>, grid, dim3(256), 0, st, a);
+  return bf16_out ? launch<__nv_bfloat16>(a, st) : launch<float>(a, st);
 }
 
 }  // namespace qkn

@@ -463,6 +463,89 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
       : "r"(taddr));
 }
 
+// ---------------------------------------------------------------- 8-bit operands, CTA pairs on one tile
+// D[tmem] (+)= A[smem] * B[smem]; kind::f8f6f4 (e4m3 inputs, fp32 accumulate), 32 columns of K.
+__device__ __forceinline__ void mma_e4m3_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The same over a pair of CTAs (cta_group::2), issued by the pair's even CTA: each CTA holds half of
+// A's rows, half of B's rows and its A rows' part of D.
+__device__ __forceinline__ void mma_e4m3_pair_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Commit of cta_group::2 operations: arrives on the mbarrier at offset `bar` in every CTA of `cta_mask`.
+__device__ __forceinline__ void mma_commit_group2_elect(uint32_t bar, uint16_t cta_mask) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+          bar),
+      "h"(cta_mask)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Tile load into this CTA's shared memory whose bytes complete on an mbarrier of either CTA of the
+// pair (`cluster_bar` from mapa_shared).
+__device__ __forceinline__ void tma_load_2d_pair_elect(uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                                       uint32_t cluster_bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(cluster_bar)
+      : "memory");
+}
+// Arrival on an mbarrier of another CTA that orders this thread's earlier operations before it.
+__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// Warp-uniform bounded wait for phases that another CTA of the cluster completes (see mbar_try_wait_cl).
+__device__ __forceinline__ bool mbar_wait_warp_cl(uint32_t bar, uint32_t parity, int64_t limit) {
+  if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
+    if (__shfl_sync(0xffffffffu, (int)(clock64() - t0 > limit), 0)) return false;
+  }
+}
+// Instruction descriptor for kind::f8f6f4 with e4m3 A/B (both K-major), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4)                     // D format: f32 (A and B formats 0: e4m3)
+         | ((uint32_t)(n >> 3) << 17)  // N / 8
+         | ((uint32_t)(m >> 4) << 24); // M / 16
+}
+// 16 bytes from another CTA's shared memory (ordered by a cluster barrier before it).
+__device__ __forceinline__ float4 ld_shared_remote_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
 // Position in a ring of N mbarrier-guarded slots: the slot and the parity of its current use.
 template <int N>
 struct RingPos {
