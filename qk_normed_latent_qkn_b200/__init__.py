@@ -341,32 +341,37 @@ def gqa_decode(dims: Dims, cache: GqaCache, q, q_rope, gamma_q, gamma_qr, block_
 
 
 # ----------------------------------------------------------------- 8-bit projections
+# (These calls take a few microseconds on the GPU for one token, so the marshalling is kept as short: plain
+# conditions, and the current stream's handle without a Stream object.)
 FP8_GROUP = 128            # columns (and, in a weight, rows) that share a scale
-
-
-def _round_up(v: int, to: int) -> int:
-    return (v + to - 1) // to * to
+_E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
+_DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32}
 
 
 class Fp8Rows:
     """Rows of ``cols`` values in 8 bits (see qkn_fp8_rows): ``codes`` float8_e4m3fn [rows, ld], ``scale`` fp32
     [ceil(cols / 128), ld_scale] with a block's scales of all rows side by side."""
 
+    __slots__ = ("codes", "scale", "rows", "cols")
+
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, cols: int):
-        _need(codes.dim() == 2 and codes.dtype == torch.float8_e4m3fn and codes.is_contiguous(),
-              "codes is a contiguous float8_e4m3fn [rows, ld]")
-        _need(scale.dim() == 2 and scale.dtype == torch.float32 and scale.is_contiguous(),
-              "scale is a contiguous float32 [ceil(cols / 128), ld_scale]")
-        _need(1 <= cols <= codes.shape[1] and scale.shape[0] == (cols + FP8_GROUP - 1) // FP8_GROUP
-              and scale.shape[1] >= codes.shape[0] and scale.device == codes.device,
-              "codes and scale hold rows of cols values, on one device")
-        self.codes, self.scale, self.rows, self.cols = codes, scale, int(codes.shape[0]), int(cols)
+        if codes.dtype != _E4M3 or codes.dim() != 2 or not codes.is_contiguous():
+            raise ValueError("codes is a contiguous float8_e4m3fn [rows, ld]")
+        if scale.dtype != _FP32 or scale.dim() != 2 or not scale.is_contiguous() or scale.device != codes.device:
+            raise ValueError("scale is a contiguous float32 [ceil(cols / 128), ld_scale] on the codes' device")
+        rows, ld = codes.shape
+        blocks, ld_scale = scale.shape
+        if not 1 <= cols <= ld or blocks != (cols + 127) // FP8_GROUP or ld_scale < rows:
+            raise ValueError("codes and scale hold rows of cols values")
+        self.codes, self.scale, self.rows, self.cols = codes, scale, rows, cols
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Fp8Rows":
-        return cls(torch.empty((rows, _round_up(cols, 16)), dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty(((cols + FP8_GROUP - 1) // FP8_GROUP, max(4, _round_up(rows, 4))),
-                               dtype=torch.float32, device=device), cols)
+        q = cls.__new__(cls)
+        q.codes = torch.empty((rows, (cols + 15) // 16 * 16), dtype=_E4M3, device=device)
+        q.scale = torch.empty(((cols + 127) // FP8_GROUP, max(4, (rows + 3) // 4 * 4)), dtype=_FP32, device=device)
+        q.rows, q.cols = rows, cols
+        return q
 
     def c(self) -> _Fp8Rows:
         return _Fp8Rows(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.codes.shape[1],
@@ -377,87 +382,104 @@ class Fp8Weight:
     """A weight in 8 bits, one row per output column (see qkn_fp8_weight): ``codes`` float8_e4m3fn [rows, ld],
     ``scale`` fp32 [ceil(rows / 128), ceil(cols / 128)]."""
 
+    __slots__ = ("codes", "scale", "rows", "cols")
+
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, cols: int):
-        _need(codes.dim() == 2 and codes.dtype == torch.float8_e4m3fn and codes.is_contiguous(),
-              "codes is a contiguous float8_e4m3fn [rows, ld]")
-        _need(1 <= cols <= codes.shape[1] and scale.dtype == torch.float32 and scale.is_contiguous()
-              and scale.device == codes.device
-              and tuple(scale.shape) == ((codes.shape[0] + FP8_GROUP - 1) // FP8_GROUP,
-                                         (cols + FP8_GROUP - 1) // FP8_GROUP),
-              "scale is a contiguous float32 [ceil(rows / 128), ceil(cols / 128)] on the codes' device")
-        self.codes, self.scale, self.rows, self.cols = codes, scale, int(codes.shape[0]), int(cols)
+        if codes.dtype != _E4M3 or codes.dim() != 2 or not codes.is_contiguous():
+            raise ValueError("codes is a contiguous float8_e4m3fn [rows, ld]")
+        rows, ld = codes.shape
+        if (not 1 <= cols <= ld or scale.dtype != _FP32 or not scale.is_contiguous() or scale.device != codes.device
+                or tuple(scale.shape) != ((rows + 127) // FP8_GROUP, (cols + 127) // FP8_GROUP)):
+            raise ValueError("scale is a contiguous float32 [ceil(rows / 128), ceil(cols / 128)] on the codes' device")
+        self.codes, self.scale, self.rows, self.cols = codes, scale, rows, cols
 
     @classmethod
     def empty(cls, rows: int, cols: int, device="cuda") -> "Fp8Weight":
-        return cls(torch.empty((rows, _round_up(cols, 16)), dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty(((rows + FP8_GROUP - 1) // FP8_GROUP, (cols + FP8_GROUP - 1) // FP8_GROUP),
-                               dtype=torch.float32, device=device), cols)
+        return cls(torch.empty((rows, (cols + 15) // 16 * 16), dtype=_E4M3, device=device),
+                   torch.empty(((rows + 127) // FP8_GROUP, (cols + 127) // FP8_GROUP), dtype=_FP32, device=device),
+                   cols)
 
     def c(self) -> _Fp8Weight:
         return _Fp8Weight(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.codes.shape[1])
 
 
-def _need(ok: bool, what: str) -> None:
-    if not ok:
-        raise ValueError(what)
+def _type_code(t: torch.Tensor, what: str) -> int:
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} is bfloat16 or float32")
+    return code
 
 
-def _dtype_code(t: torch.Tensor, what: str) -> int:
-    _need(t.dtype in (torch.bfloat16, torch.float32), f"{what} is bfloat16 or float32")
-    return BF16 if t.dtype == torch.bfloat16 else F32
+def _call_on(device: torch.device, stream, fn, *args) -> int:
+    """``fn(*args, stream handle)`` with ``device`` current: the library launches on the current device."""
+    if device.type != "cuda":
+        return fn(*args, _stream(stream))
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return fn(*args, _stream(stream))
+    return fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream))
 
 
-def _call_on(device: torch.device, stream, call) -> int:
-    """``call(stream handle)`` with ``device`` current: the library launches on the current device."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+def _beside(t: Optional[torch.Tensor], x: torch.Tensor, what: str) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype != x.dtype or t.shape != x.shape or not t.is_contiguous() or t.device != x.device:
+        raise ValueError(f"{what} is dense, of x's shape, type and device")
+    return t.data_ptr()
 
 
 def norm_quant(x, q: Fp8Rows, gamma=None, eps: float = 1e-6, residual=None, residual_out=None, y=None,
                stream=None) -> None:
     """Residual addition, RMSNorm (with ``gamma``) and quantisation of rows to 8 bits (see qkn_norm_quant): ``x``
     [n, d], its rows contiguous; ``residual`` / ``residual_out`` / ``y`` dense [n, d] of x's type or None."""
-    _need(x.dim() == 2 and (x.stride(1) == 1 or x.shape[1] == 1), "x is [n, d] with contiguous rows")
-    n, d = int(x.shape[0]), int(x.shape[1])
-    _need((q.rows, q.cols) == (n, d), "q holds n rows of d values")
-    for t, what in ((residual, "residual"), (residual_out, "residual_out"), (y, "y")):
-        _need(t is None or (t.dtype == x.dtype and tuple(t.shape) == (n, d) and t.is_contiguous()
-                            and t.device == x.device), f"{what} is a dense [n, d] of x's type and device")
-    _need(gamma is None or (gamma.dtype == torch.float32 and tuple(gamma.shape) == (d,) and gamma.is_contiguous()
-                            and gamma.device == x.device), "gamma is a float32 [d] on x's device")
-    _need(q.codes.device == x.device, "q is on x's device")
-    ld_x = int(x.stride(0)) if n > 1 else d
-    _check(_call_on(x.device, stream, lambda st: _lib.qkn_norm_quant(
-        _dtype_code(x, "x"), _ptr(x), ld_x, _ptr(residual), _ptr(gamma), eps, _ptr(residual_out), _ptr(y),
-        ctypes.byref(q.c()), st)), "qkn_norm_quant")
+    dtype, dev = _type_code(x, "x"), x.device
+    if x.dim() != 2:
+        raise ValueError("x is [n, d] with contiguous rows")
+    n, d = x.shape
+    ld_x, step = x.stride()
+    if step != 1 and d != 1:
+        raise ValueError("x is [n, d] with contiguous rows")
+    if q.rows != n or q.cols != d or q.codes.device != dev:
+        raise ValueError("q holds n rows of d values on x's device")
+    g = None
+    if gamma is not None:
+        if gamma.dtype != _FP32 or gamma.shape != (d,) or not gamma.is_contiguous() or gamma.device != dev:
+            raise ValueError("gamma is a float32 [d] on x's device")
+        g = gamma.data_ptr()
+    _check(_call_on(dev, stream, _lib.qkn_norm_quant, dtype, x.data_ptr(), ld_x if n > 1 else d,
+                    _beside(residual, x, "residual"), g, eps, _beside(residual_out, x, "residual_out"),
+                    _beside(y, x, "y"), ctypes.byref(q.c())), "qkn_norm_quant")
 
 
 def quant_weight(w, q: Fp8Weight, stream=None) -> None:
     """Quantise a dense weight [n, k] to 8 bits with a scale for each block of 128 x 128 (see qkn_quant_weight)."""
-    _need(w.dim() == 2 and w.is_contiguous() and (q.rows, q.cols) == tuple(w.shape) and q.codes.device == w.device,
-          "w is a dense [n, k], q holds as much on its device")
-    _check(_call_on(w.device, stream, lambda st: _lib.qkn_quant_weight(_dtype_code(w, "w"), _ptr(w),
-                                                                       ctypes.byref(q.c()), st)), "qkn_quant_weight")
+    dtype, dev = _type_code(w, "w"), w.device
+    if w.shape != (q.rows, q.cols) or not w.is_contiguous() or q.codes.device != dev:
+        raise ValueError("w is a dense [n, k], q holds as much on its device")
+    _check(_call_on(dev, stream, _lib.qkn_quant_weight, dtype, w.data_ptr(), ctypes.byref(q.c())),
+           "qkn_quant_weight")
 
 
 def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=None) -> None:
     """out = A W^T from 8 bits (see qkn_fp8_linear); ``outs``: up to MAX_OUTS tensors [a.rows, width] of one type,
     their rows contiguous, that take the product's columns in order."""
-    _need(1 <= len(outs) <= MAX_OUTS, f"outs holds 1 to {MAX_OUTS} tensors")
-    dev = a.codes.device
-    arr = (_OutCols * len(outs))()
-    for i, t in enumerate(outs):
-        _need(t.dim() == 2 and t.shape[0] == a.rows and (t.stride(1) == 1 or t.shape[1] == 1)
-              and t.dtype == outs[0].dtype and t.device == dev,
-              "an output is [rows, width] with contiguous rows, all of one type, on the codes' device")
-        width = int(t.shape[1])
-        arr[i] = _OutCols(t.data_ptr(), width, int(t.stride(0)) if a.rows > 1 else width)
-    _need(w.codes.device == dev and workspace.device == dev, "all tensors are on one device")
-    _check(_call_on(dev, stream, lambda st: _lib.qkn_fp8_linear(
-        ctypes.byref(a.c()), ctypes.byref(w.c()), _dtype_code(outs[0], "outs"), len(outs), arr, _ptr(workspace),
-        workspace.numel() * workspace.element_size(), st)), "qkn_fp8_linear")
+    n_outs, dev, rows = len(outs), a.codes.device, a.rows
+    if not 1 <= n_outs <= MAX_OUTS:
+        raise ValueError(f"outs holds 1 to {MAX_OUTS} tensors")
+    dtype = _type_code(outs[0], "outs")
+    arr = (_OutCols * n_outs)()
+    for t, o in zip(outs, arr):
+        if t.dim() != 2 or t.shape[0] != rows or t.dtype != outs[0].dtype or t.device != dev:
+            raise ValueError("an output is [rows, width], all of one type, on the codes' device")
+        ld, step = t.stride()
+        width = t.shape[1]
+        if step != 1 and width != 1:
+            raise ValueError("an output's rows are contiguous")
+        o.out, o.cols, o.ld = t.data_ptr(), width, ld if rows > 1 else width
+    if w.codes.device != dev or workspace.device != dev:
+        raise ValueError("all tensors are on one device")
+    _check(_call_on(dev, stream, _lib.qkn_fp8_linear, ctypes.byref(a.c()), ctypes.byref(w.c()), dtype, n_outs, arr,
+                    workspace.data_ptr(), workspace.nbytes), "qkn_fp8_linear")
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:
