@@ -241,7 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (c == 6) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_release(mapa_shared(smem_u32(&bars.t_empty[acc.slot]), 0));
+            // (relaxed: the sums are in registers, and a release would wait for the scales' loads too)
+            if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&bars.t_empty[acc.slot]), 0));
           }
         }
         acc.next();

@@ -517,10 +517,6 @@ __device__ __forceinline__ void tma_load_2d_pair_elect(uint32_t dst, const void*
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
-// Arrival on an mbarrier of another CTA that orders this thread's earlier operations before it.
-__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
 // Warp-uniform bounded wait for phases that another CTA of the cluster completes (see mbar_try_wait_cl).
 __device__ __forceinline__ bool mbar_wait_warp_cl(uint32_t bar, uint32_t parity, int64_t limit) {
   if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
