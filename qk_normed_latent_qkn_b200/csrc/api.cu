@@ -685,7 +685,7 @@ bool check_dtype(qkn_dtype t) { return t == QKN_F32 || t == QKN_BF16; }
 
 // Codes and scales of `rows` rows of `cols` values each (a weight's scales are dense, ld_scale = 0 here).
 bool check_fp8(const void* codes, const float* scale, int32_t rows, int32_t cols, int64_t ld, int64_t ld_scale) {
-  if (rows < 0 || cols < 1 || cols > (1 << 30) || ld < cols || ld % 16 || ld > (int64_t{1} << 32)) return false;
+  if (rows < 0 || rows > (1 << 30) || cols < 1 || cols > (1 << 30) || ld < cols || ld % 16 || ld > (int64_t{1} << 32)) return false;
   if ((rows > 0 && (!codes || !scale)) || !aligned(codes, 16)) return false;
   if (ld_scale == 0) return aligned(scale, 4);
   return ld_scale >= rows && ld_scale % 4 == 0 && ld_scale <= (int64_t{1} << 32) && aligned(scale, 16);

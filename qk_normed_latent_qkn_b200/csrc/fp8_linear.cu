@@ -40,79 +40,95 @@ __device__ __forceinline__ bool wide_ok(const OutCols& o) {
   return (reinterpret_cast<uintptr_t>(o.out) & 15) == 0 && o.ld % E == 0 && o.begin % E == 0;
 }
 
-// N (a multiple of 8) consecutive columns of one row, from column col of the product.
-template <typename O, int N>
-__device__ __forceinline__ void store_cols(const Fp8LinearArgs& p, int64_t row, int col, const float (&v)[N]) {
-  if (col >= p.n) return;
-  int o = 0;
-  while (col >= p.outs[o].end) ++o;
-  if (col + N <= p.outs[o].end && wide_ok<O>(p.outs[o])) {
-    O* dst = static_cast<O*>(p.outs[o].out) + row * p.outs[o].ld + (col - p.outs[o].begin);
-    if constexpr (sizeof(O) == 4) {
-#pragma unroll
-      for (int e = 0; e < N; e += 4)
-        *reinterpret_cast<float4*>(dst + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; e += 8) {
-        uint4 u;
-        __nv_bfloat162 t[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(v[e + 2 * i], v[e + 2 * i + 1]);
-        u.x = *reinterpret_cast<uint32_t*>(&t[0]);
-        u.y = *reinterpret_cast<uint32_t*>(&t[1]);
-        u.z = *reinterpret_cast<uint32_t*>(&t[2]);
-        u.w = *reinterpret_cast<uint32_t*>(&t[3]);
-        *reinterpret_cast<uint4*>(dst + e) = u;
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    if (col + e >= p.n) return;
-    while (col + e >= p.outs[o].end) ++o;
-    static_cast<O*>(p.outs[o].out)[row * p.outs[o].ld + (col + e - p.outs[o].begin)] = from_f32<O>(v[e]);
-  }
+// A load that stays where it is written: the compiler would move an ordinary one down to its use.
+__device__ __forceinline__ float load_early(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
 }
 
-// Packed pairs of fp32 (the sm_100 FMA takes two at a time).
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-  return r;
+// One warp's 32 rows x 256 / sizeof(O) columns of the product pass through `box` (8 KB of shared memory)
+// from lanes that hold a row each to lanes that write 256 consecutive bytes of a row: straight from the
+// registers every lane's 16 bytes would be a half-written sector of another row.  The 16-byte pieces of
+// row r are permuted by r % 8, which keeps both sides free of bank conflicts.
+constexpr int kBoxRow = 256, kBoxBytes = 32 * kBoxRow;
+
+template <typename O>
+__device__ __forceinline__ void fill_box(uint8_t* box, const float* v) {
+  constexpr int E = 16 / (int)sizeof(O);
+  const int lane = threadIdx.x & 31;
+  uint8_t* row = box + lane * kBoxRow;
+#pragma unroll
+  for (int u = 0; u < 16; ++u) {
+    uint4 w;
+    if constexpr (sizeof(O) == 4) {
+      w = make_uint4(__float_as_uint(v[u * E]), __float_as_uint(v[u * E + 1]), __float_as_uint(v[u * E + 2]),
+                     __float_as_uint(v[u * E + 3]));
+    } else {
+      __nv_bfloat162 t[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) t[i] = __floats2bfloat162_rn(v[u * E + 2 * i], v[u * E + 2 * i + 1]);
+      w = make_uint4(*reinterpret_cast<uint32_t*>(&t[0]), *reinterpret_cast<uint32_t*>(&t[1]),
+                     *reinterpret_cast<uint32_t*>(&t[2]), *reinterpret_cast<uint32_t*>(&t[3]));
+    }
+    *reinterpret_cast<uint4*>(row + ((u ^ (lane & 7)) << 4)) = w;
+  }
+  __syncwarp();
 }
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+
+template <typename O>
+__device__ __forceinline__ void write_box(const Fp8LinearArgs& p, const uint8_t* box, int row0, int col0) {
+  constexpr int E = 16 / (int)sizeof(O), COLS = 16 * E;
+  const int lane = threadIdx.x & 31;
+  if (col0 < p.n) {
+    int o = 0;
+    while (col0 >= p.outs[o].end) ++o;
+    const int rows = min(32, p.m - row0);
+    if (col0 + COLS <= p.outs[o].end && wide_ok<O>(p.outs[o])) {
+      O* dst = static_cast<O*>(p.outs[o].out) + (col0 - p.outs[o].begin) + (lane & 15) * E;
+      for (int r = lane >> 4; r < rows; r += 2)
+        *reinterpret_cast<uint4*>(dst + (row0 + r) * p.outs[o].ld) =
+            *reinterpret_cast<const uint4*>(box + r * kBoxRow + (((lane & 15) ^ (r & 7)) << 4));
+    } else {   // a destination ends inside the box, or its rows are not 16-byte aligned: element by element
+      for (int e = lane; e < COLS && col0 + e < p.n; e += 32) {
+        while (col0 + e >= p.outs[o].end) ++o;
+        O* dst = static_cast<O*>(p.outs[o].out) + (col0 + e - p.outs[o].begin);
+        for (int r = 0; r < rows; ++r)
+          dst[(row0 + r) * p.outs[o].ld] =
+              *reinterpret_cast<const O*>(box + r * kBoxRow + (((e / E) ^ (r & 7)) << 4) + (e % E) * sizeof(O));
+      }
+    }
+  }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- many rows: CTA pairs
 constexpr int kPairM = 256, kPairN = 256;       // tile of a pair
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kPairStageBytes = 2 * kTileBytes; // this CTA's 128 rows of A and 128 of W
-constexpr int kPairThreads = 320;               // producer, MMA, 8 epilogue warps
+constexpr int kPairWarps = 8;                   // epilogue warps, each 32 rows x 128 columns
+constexpr int kPairThreads = 64 + 32 * kPairWarps;
+constexpr int kPairCols = 128;                  // columns of an epilogue warp
 constexpr int kPairGroupM = 16;                 // row tiles that are walked before the next column tile
+constexpr int kLoadCols = 16;                   // columns of one TMEM load
+
 
 struct PairBars {
   uint64_t full[kPairStages], empty[kPairStages];
   uint64_t t_full[2], t_empty[2];
   uint32_t tmem;
 };
-constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 1024;
+constexpr int kPairBoxOff = kPairStages * kPairStageBytes;
+constexpr int kPairBarOff = kPairBoxOff + kPairWarps * kBoxBytes;
+constexpr int kPairSmem = 1024 + kPairBarOff + (int)sizeof(PairBars);
+static_assert(kPairSmem <= 227 * 1024, "shared memory of a CTA");
 
 struct TileWalk {
   int mt, nt;
-  __device__ __forceinline__ void of(int64_t t, int& m, int& n) const {
-    const int64_t per = (int64_t)kPairGroupM * nt;
-    const int g = (int)(t / per);
+  __device__ __forceinline__ void of(int t, int& m, int& n) const {
+    const int g = t / (kPairGroupM * nt);
     const int rows = min(kPairGroupM, mt - g * kPairGroupM);
-    const int r = (int)(t - (int64_t)g * per);
+    const int r = t - g * kPairGroupM * nt;
     m = g * kPairGroupM + r % rows;
     n = r / rows;
   }
@@ -125,7 +141,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ Fp8LinearArgs p, const __grid_constant__ LinearMaps maps) {
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
-  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairStages * kPairStageBytes);
+  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairBarOff);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t stages = smem_u32(smem);
@@ -137,7 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&bars.t_full[i]), 1);
-      mbar_init(smem_u32(&bars.t_empty[i]), 16);   // 8 epilogue warps of each CTA
+      mbar_init(smem_u32(&bars.t_empty[i]), 2 * kPairWarps);   // of both CTAs
     }
     mbar_fence_init();
     prefetch_tmap(&maps.a);
@@ -156,19 +172,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_wait();
 
   const TileWalk walk{(p.m + kPairM - 1) / kPairM, (p.n + kPairN - 1) / kPairN};
-  const int64_t tiles = (int64_t)walk.mt * walk.nt;
+  const int tiles = walk.mt * walk.nt;   // (the launcher checks that they fit)
   const int blocks = (p.k + kFp8Group - 1) / kFp8Group;
   const int pairs = gridDim.x >> 1;
   bool ok = true;
 
   if (warp == 0) {
     RingPos<kPairStages> ring;
-    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+    for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
       int m, n;
       walk.of(t, m, n);
       const int y_a = m * kPairM + (int)rank * 128, y_w = n * kPairN + (int)rank * 128;
       for (int b = 0; b < blocks; ++b) {
-        if (!mbar_wait_warp_cl(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
+        if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
         const uint32_t full = smem_u32(&bars.full[ring.slot]);
         if (rank == 0) mbar_arrive_expect_tx_elect(full, 2 * kPairStageBytes);
         const uint32_t dst = stages + ring.slot * kPairStageBytes;
@@ -180,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     // the last uses of the stages end before this CTA does: their commits arrive here
     for (int i = 0; i < kPairStages; ++i) {
-      if (!mbar_wait_warp_cl(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
+      if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
       ring.next();
     }
   } else if (warp == 1 && rank == 0) {
@@ -188,10 +204,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const uint64_t d_a = smem_desc(stages, 16, 1024), d_w = smem_desc(stages + kTileBytes, 16, 1024);
     RingPos<kPairStages> ring;
     RingPos<2> acc;
-    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs)
+    for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs)
       for (int b = 0; b < blocks; ++b) {
-        if (!mbar_wait_warp_cl(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles) ||
-            !mbar_wait_warp_cl(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles)) {
+        if (!mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles) ||
+            !mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles)) {
           ok = false;
           break;
         }
@@ -208,53 +224,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
   } else if (warp >= 2) {
     const int quad = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* box = smem + kPairBoxOff + (warp - 2) * kBoxBytes;
+    const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + half * kPairCols;
     RingPos<2> acc;
-    for (int64_t t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+    float total[kPairCols];
+    // One block of K: its sums leave TMEM 16 columns at a time, the next ones on their way while these
+    // enter the total.  (Single FMAs: as packed pairs they need the same FMA cycles and, with the moves
+    // that pair up registers, more instructions.)
+    auto enter = [&](float s) {
+      if (ok && !mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) ok = false;
+      tc_fence_after();
+      const uint32_t at = tq + acc.slot * kPairN;
+      constexpr int N = kPairCols / kLoadCols;
+      uint32_t v[2][kLoadCols];
+      tmem_ld16(at, v[0]);
+      tmem_wait_ld(v[0]);
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if (c < N - 1) tmem_ld16(at + (c + 1) * kLoadCols, v[(c + 1) & 1]);
+#pragma unroll
+        for (int e = 0; e < kLoadCols; ++e)
+          total[c * kLoadCols + e] = fmaf(__uint_as_float(v[c & 1][e]), s, total[c * kLoadCols + e]);
+        if (c < N - 1) tmem_wait_ld(v[(c + 1) & 1]);
+        if (c == N - 2) {   // everything is out of TMEM
+          tc_fence_before();
+          __syncwarp();
+          // (relaxed: what the arrival stands for, the loads from TMEM, is complete, and a release would
+          // wait for the scales' loads too)
+          if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&bars.t_empty[acc.slot]), 0));
+        }
+      }
+      acc.next();
+    };
+    // The scales of a tile's blocks, one of this lane's row and one of the warp's 128 columns, are asked
+    // for two blocks ahead.
+    for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
       int m, n;
       walk.of(t, m, n);
-      const int row = m * kPairM + (int)rank * 128 + quad * 32 + lane;
-      const int col = n * kPairN + half * 128;
-      const float* sa = p.a_scale + min(row, p.m - 1);
-      const float* sw = p.w_scale + (int64_t)min(col / kFp8Group, (p.n - 1) / kFp8Group) * blocks;
-      uint64_t total[64];
+      const float* sa = p.a_scale + min(m * kPairM + (int)rank * 128 + quad * 32 + lane, p.m - 1);
+      const float* sw = p.w_scale + (int64_t)min(2 * n + half, (p.n - 1) / kFp8Group) * blocks;
+      const int b1 = blocks > 1 ? 1 : 0;
+      float s0 = __ldg(sa) * __ldg(sw), s1 = __ldg(sa + b1 * p.ld_as) * __ldg(sw + b1);
 #pragma unroll
-      for (int i = 0; i < 64; ++i) total[i] = 0;
-      // the next block's scales are on their way while this one's sums are entered
-      float s_next = __ldg(sa) * __ldg(sw);
-      for (int b = 0; b < blocks; ++b) {
-        const float s = s_next;
-        const int bn = min(b + 1, blocks - 1);
-        const float sa_n = __ldg(sa + bn * p.ld_as), sw_n = __ldg(sw + bn);
-        if (!mbar_wait_warp_cl(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) { ok = false; break; }
-        tc_fence_after();
-        const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc.slot * kPairN + half * 128;
-        const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
-        uint32_t v[2][16];
-        tmem_ld16(at, v[0]);
-        tmem_wait_ld(v[0]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          if (c < 7) tmem_ld16(at + (c + 1) * 16, v[(c + 1) & 1]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) fma2(total[c * 8 + e], pack2(v[c & 1][2 * e], v[c & 1][2 * e + 1]), s2);
-          if (c < 7) tmem_wait_ld(v[(c + 1) & 1]);
-          if (c == 6) {
-            tc_fence_before();
-            __syncwarp();
-            // (relaxed: the sums are in registers, and a release would wait for the scales' loads too)
-            if (lane == 0) mbar_arrive_remote(mapa_shared(smem_u32(&bars.t_empty[acc.slot]), 0));
-          }
-        }
-        acc.next();
-        s_next = sa_n * sw_n;
+      for (int i = 0; i < kPairCols; ++i) total[i] = 0.f;
+      for (int b = 0; b < blocks; b += 2) {
+        const int b2 = min(b + 2, blocks - 1), b3 = min(b + 3, blocks - 1);
+        const float a2 = load_early(sa + b2 * p.ld_as), w2 = load_early(sw + b2);
+        enter(s0);
+        const float a3 = load_early(sa + b3 * p.ld_as), w3 = load_early(sw + b3);
+        if (b + 1 < blocks) enter(s1);
+        s0 = a2 * w2;
+        s1 = a3 * w3;
       }
-      if (ok && row < p.m) {
+      if (ok) {
+        walk.of(t, m, n);
+        constexpr int COLS = kBoxRow / (int)sizeof(O);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float v[16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) unpack2(total[c * 8 + e], v[2 * e], v[2 * e + 1]);
-          store_cols<O>(p, row, col + c * 16, v);
+        for (int c = 0; c < kPairCols; c += COLS) {
+          fill_box<O>(box, total + c);
+          write_box<O>(p, box, m * kPairM + (int)rank * 128 + quad * 32, n * kPairN + half * kPairCols + c);
         }
       }
     }
@@ -498,6 +526,7 @@ cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   });
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)ceil_div(a.m, kPairM) * ceil_div(a.n, kPairN);
+  if (tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
   return launch_chained(linear_pair_kernel<O>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, a, maps);
 }

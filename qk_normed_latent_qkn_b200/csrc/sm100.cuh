@@ -517,15 +517,6 @@ __device__ __forceinline__ void tma_load_2d_pair_elect(uint32_t dst, const void*
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
-// Warp-uniform bounded wait for phases that another CTA of the cluster completes (see mbar_try_wait_cl).
-__device__ __forceinline__ bool mbar_wait_warp_cl(uint32_t bar, uint32_t parity, int64_t limit) {
-  if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (__all_sync(0xffffffffu, mbar_try_wait_cl(bar, parity))) return true;
-    if (__shfl_sync(0xffffffffu, (int)(clock64() - t0 > limit), 0)) return false;
-  }
-}
 // Instruction descriptor for kind::f8f6f4 with e4m3 A/B (both K-major), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4)                     // D format: f32 (A and B formats 0: e4m3)
