@@ -9,8 +9,10 @@
 // behind the last row or column, so no size needs to be a multiple of anything):
 //   * linear_pair_kernel, many rows: pairs of CTAs share a tile of 256 rows x 256 columns
 //     (cta_group::2), persistent over the tiles;
-//   * linear_split_kernel, few rows: the weight's 128 columns take the tensor core's M, the rows its N
-//     (16 to 128), and a cluster of up to 8 CTAs splits K and joins through distributed shared memory.
+//   * linear_split_kernel, few tiles: a tile is 128 columns of the product x 16 to 128 rows.  Up to 64
+//     rows the weight's columns take the tensor core's M and the rows its N; 128 rows take M themselves,
+//     because a row's scale is then one factor of the lane's.  A cluster of up to 8 CTAs splits K and
+//     joins through distributed shared memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -34,10 +36,10 @@ constexpr int kTileBytes = 128 * kRowBytes;     // 128 rows of a tile
 constexpr int kKStep = 32;                      // K of one MMA
 constexpr uint32_t kDescStep = kKStep >> 4;     // the same in descriptor units
 
-template <typename O>
+// Whether runs of E columns that start at multiples of E can be written as one piece.
+template <typename O, int E>
 __device__ __forceinline__ bool wide_ok(const OutCols& o) {
-  constexpr int E = 16 / (int)sizeof(O);
-  return (reinterpret_cast<uintptr_t>(o.out) & 15) == 0 && o.ld % E == 0 && o.begin % E == 0;
+  return reinterpret_cast<uintptr_t>(o.out) % (E * sizeof(O)) == 0 && o.ld % E == 0 && o.begin % E == 0;
 }
 
 // A load that stays where it is written: the compiler would move an ordinary one down to its use.
@@ -84,7 +86,7 @@ __device__ __forceinline__ void write_box(const Fp8LinearArgs& p, const uint8_t*
     int o = 0;
     while (col0 >= p.outs[o].end) ++o;
     const int rows = min(32, p.m - row0);
-    if (col0 + COLS <= p.outs[o].end && wide_ok<O>(p.outs[o])) {
+    if (col0 + COLS <= p.outs[o].end && wide_ok<O, E>(p.outs[o])) {
       O* dst = static_cast<O*>(p.outs[o].out) + (col0 - p.outs[o].begin) + (lane & 15) * E;
       for (int r = lane >> 4; r < rows; r += 2)
         *reinterpret_cast<uint4*>(dst + (row0 + r) * p.outs[o].ld) =
@@ -300,15 +302,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 // ---------------------------------------------------------------- few rows: K split over a cluster
 template <int NT>
 struct SplitCfg {
-  static constexpr int kStageBytes = kTileBytes + NT * kRowBytes + 1024;  // weight, rows, the rows' scales
-  static constexpr int kStages = NT == 128 ? 3 : NT == 64 ? 4 : 5;
+  static constexpr bool kRows = NT == 128;                               // the rows take the tensor core's M
+  static constexpr int kWarps = NT == 128 ? 8 : 4;                        // epilogue warps, each 32 lanes x
+  static constexpr int kPart = NT * 4 / kWarps;                          // kPart columns of the accumulator
+  static constexpr int kPitch = kRows ? 132 : 128;                       // floats of a row of partial sums
+  static constexpr int kThreads = 64 + 32 * kWarps;                       // (and the producer, the MMA)
+  static constexpr int kPerSm = NT == 128 ? 1 : 2;                       // CTAs on an SM (registers, shared memory)
+  static constexpr int kStageBytes = kTileBytes + NT * kRowBytes;         // weight, rows
+  static constexpr int kStages = NT == 128 ? 6 : NT == 64 ? 4 : 5;
   static constexpr int kCols = NT < 32 ? 32 : NT;                        // TMEM columns of one accumulator
-  static constexpr int kAccs = NT == 128 ? 2 : 4;
-  static constexpr int kBarOff = kStages * kStageBytes;
-  static constexpr int kSmem = 1024 + kBarOff + 256;
-  static constexpr int kThreads = 192;                                    // producer, MMA, 4 epilogue warps
-  static_assert(NT * 128 * 4 <= kBarOff, "the partial sums reuse the stages");
-  static_assert(kTileBytes % 1024 == 0 && (NT * kRowBytes) % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
+  static constexpr int kAccs = 4;
+  // The rows' scales have a ring of their own, so that a stage is free as soon as the tensor core has
+  // read it.  Its slots need no "empty" barrier: block b is loaded after the MMAs of block b - kStages
+  // were issued, hence after the epilogue has left block b - kStages - kAccs.
+  static constexpr int kScaleSlots = 16;
+  static constexpr int kScaleBytes = NT * 4 < 128 ? 128 : NT * 4;        // a slot; copies land on 128-byte boundaries
+  static_assert(kScaleSlots > kStages + kAccs, "scale slots are reused too early");
+  static constexpr int kScaleOff = kStages * kStageBytes;
+  static constexpr int kBarOff = kScaleOff + kScaleSlots * kScaleBytes;
+  static constexpr int kSmem = 1024 + kBarOff + 512;
+  static_assert(kSmem * kPerSm <= (227 - kPerSm) * 1024, "shared memory of an SM");
+  static_assert(NT * kPitch * 4 <= kScaleOff, "the partial sums reuse the stages");
+  static_assert(kScaleOff % 128 == 0 && kScaleBytes % 128 == 0, "a copy's destination");
+  static_assert(kTileBytes % 1024 == 0 && kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
 template <int S, int A>
@@ -319,15 +335,16 @@ struct SplitBars {
 };
 
 // One tile: 128 columns of the product for NT rows.  Cluster rank r takes the r-th part of K's blocks.
-// Warps: 0 producer, 1 MMA, 2-5 epilogue.
+// Warps: 0 producer, 1 MMA, 2 on: epilogue.
 template <int NT, typename O>
-__global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant__ Fp8LinearArgs p,
+__global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(const __grid_constant__ Fp8LinearArgs p,
                                                            const __grid_constant__ LinearMaps maps, int split,
                                                            int row_tiles) {
   using C = SplitCfg<NT>;
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
   auto& bars = *reinterpret_cast<SplitBars<C::kStages, C::kAccs>*>(smem + C::kBarOff);
+  static_assert(sizeof(bars) <= 512, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = blockIdx.x % split;                     // (clusters lie along x)
   const int tile = blockIdx.x / split;
@@ -340,11 +357,11 @@ __global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&bars.full[i]), 1);
-      mbar_init(smem_u32(&bars.empty[i]), 5);              // the MMA's commit and the 4 epilogue warps
+      mbar_init(smem_u32(&bars.empty[i]), 1);
     }
     for (int i = 0; i < C::kAccs; ++i) {
-      mbar_init(smem_u32(&bars.t_full[i]), 1);
-      mbar_init(smem_u32(&bars.t_empty[i]), 4);
+      mbar_init(smem_u32(&bars.t_full[i]), 2);             // the MMA warp, and its MMAs when they are done
+      mbar_init(smem_u32(&bars.t_empty[i]), C::kWarps);
     }
     mbar_fence_init();
     prefetch_tmap(&maps.a);
@@ -363,26 +380,29 @@ __global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant
   pdl_wait();
 
   bool ok = true;
-  float total[NT];
+  float total[C::kPart];
   if (warp == 0) {
     RingPos<C::kStages> ring;
+    RingPos<C::kScaleSlots> sring;
     for (int b = b0; b < b1; ++b) {
       if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
       const uint32_t full = smem_u32(&bars.full[ring.slot]);
       const uint32_t dst = stages + ring.slot * C::kStageBytes;
-      mbar_arrive_expect_tx_elect(full, kTileBytes + NT * kRowBytes + NT * 4);
+      mbar_arrive_expect_tx_elect(full, C::kStageBytes + NT * 4);
       tma_load_2d_elect(dst, &maps.w, b * kFp8Group, n0, full);
       tma_load_2d_elect(dst + kTileBytes, &maps.a, b * kFp8Group, row0, full);
-      tma_load_2d_elect(dst + kTileBytes + NT * kRowBytes, &maps.a_scale, row0, b, full);
+      tma_load_2d_elect(stages + C::kScaleOff + sring.slot * C::kScaleBytes, &maps.a_scale, row0, b, full);
       ring.next();
+      sring.next();
     }
     for (int i = 0; i < C::kStages; ++i) {                  // nothing of this CTA's is in flight after this
-      if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
+      if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
       ring.next();
     }
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_e4m3(128, NT);
     const uint64_t d_w = smem_desc(stages, 16, 1024), d_a = smem_desc(stages + kTileBytes, 16, 1024);
+    const uint64_t d_m = C::kRows ? d_a : d_w, d_n = C::kRows ? d_w : d_a;
     RingPos<C::kStages> ring;
     RingPos<C::kAccs> acc;
     for (int b = b0; b < b1; ++b) {
@@ -395,53 +415,54 @@ __global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant
       const uint64_t at = (uint64_t)((ring.slot * C::kStageBytes) >> 4);
 #pragma unroll
       for (int s = 0; s < kFp8Group / kKStep; ++s)
-        mma_e4m3_elect(tmem + acc.slot * C::kCols, d_w + at + s * kDescStep, d_a + at + s * kDescStep, idesc, s > 0);
+        mma_e4m3_elect(tmem + acc.slot * C::kCols, d_m + at + s * kDescStep, d_n + at + s * kDescStep, idesc, s > 0);
       mma_commit_elect(smem_u32(&bars.empty[ring.slot]));
       mma_commit_elect(smem_u32(&bars.t_full[acc.slot]));
+      mbar_arrive_elect(smem_u32(&bars.t_full[acc.slot]));   // passes on the scales, which came with the stage
       ring.next();
       acc.next();
     }
   } else {
-    const int quad = warp & 3;
+    const int quad = warp & 3, part = (warp - 2) >> 2;
     const float* sw = p.w_scale + (int64_t)(n0 / kFp8Group) * blocks;
-    RingPos<C::kStages> ring;
+    RingPos<C::kScaleSlots> sring;
     RingPos<C::kAccs> acc;
 #pragma unroll
-    for (int i = 0; i < NT; ++i) total[i] = 0.f;
-    float sw_next = b0 < b1 ? __ldg(sw + b0) : 0.f;
+    for (int i = 0; i < C::kPart; ++i) total[i] = 0.f;
+    float sw_lane = 0.f;             // the weight's scales of 32 blocks, one per lane
     for (int b = b0; b < b1; ++b) {
-      const float s = sw_next;
-      sw_next = __ldg(sw + min(b + 1, b1 - 1));
-      // the rows' scales are ordinary reads of what the copy wrote: wait for its barrier too
-      if (!mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles) ||
-          !mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) {
-        ok = false;
-        break;
-      }
+      if (((b - b0) & 31) == 0) sw_lane = __ldg(sw + min(b + lane, b1 - 1));
+      const float s = __shfl_sync(0xffffffffu, sw_lane, (b - b0) & 31);
+      if (!mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) { ok = false; break; }
       tc_fence_after();
-      const float4* sa = reinterpret_cast<const float4*>(smem + ring.slot * C::kStageBytes + kTileBytes + NT * kRowBytes);
-      const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc.slot * C::kCols;
+      const uint8_t* sa = smem + C::kScaleOff + sring.slot * C::kScaleBytes;
+      const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc.slot * C::kCols + part * C::kPart;
+      // 16 sums at a time; the factors are formed, and the next sums asked for, while these are on their way
+      uint32_t v[2][16];
+      tmem_ld16(at, v[0]);
+      const float row_f = C::kRows ? reinterpret_cast<const float*>(sa)[quad * 32 + lane] * s : 0.f;
 #pragma unroll
-      for (int c = 0; c < NT; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(at + c, v);
-        tmem_wait_ld(v);
+      for (int c = 0; c < C::kPart; c += 16) {
+        uint32_t(&u)[16] = v[(c >> 4) & 1];
+        float f[16];
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
-          const float4 f = sa[(c + e) >> 2];
-          total[c + e] += __uint_as_float(v[e]) * (f.x * s);
-          total[c + e + 1] += __uint_as_float(v[e + 1]) * (f.y * s);
-          total[c + e + 2] += __uint_as_float(v[e + 2]) * (f.z * s);
-          total[c + e + 3] += __uint_as_float(v[e + 3]) * (f.w * s);
+          if constexpr (C::kRows) {
+            f[e] = f[e + 1] = f[e + 2] = f[e + 3] = row_f;
+          } else {
+            const float4 q = reinterpret_cast<const float4*>(sa)[(c + e) >> 2];
+            f[e] = q.x * s, f[e + 1] = q.y * s, f[e + 2] = q.z * s, f[e + 3] = q.w * s;
+          }
         }
+        tmem_wait_ld(u);
+        if (c + 16 < C::kPart) tmem_ld16(at + c + 16, v[((c >> 4) & 1) ^ 1]);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) total[c + e] = fmaf(__uint_as_float(u[e]), f[e], total[c + e]);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&bars.t_empty[acc.slot]));
-        mbar_arrive(smem_u32(&bars.empty[ring.slot]));
-      }
-      ring.next();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[acc.slot]));
+      sring.next();
       acc.next();
     }
   }
@@ -453,17 +474,31 @@ __global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols * C::kAccs);
   }
-  float* part = reinterpret_cast<float*>(smem);             // [rows][128]
+  float* sums = reinterpret_cast<float*>(smem);             // [rows][kPitch]
   if (warp >= 2) {
-    const int c = (warp & 3) * 32 + lane;
+    const int i = (warp & 3) * 32 + lane, j0 = ((warp - 2) >> 2) * C::kPart;   // this thread's TMEM lane and columns
+    if constexpr (C::kRows) {
+      if (i < rows) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      if (j < rows) part[j * 128 + c] = total[j];
+        for (int j = 0; j < C::kPart; j += 4)
+          *reinterpret_cast<float4*>(sums + i * C::kPitch + j0 + j) =
+              make_float4(total[j], total[j + 1], total[j + 2], total[j + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < C::kPart; ++j)
+        if (j0 + j < rows) sums[(j0 + j) * C::kPitch + i] = total[j];
+    }
   }
   cluster_sync();
   // rank r joins and writes the rows r, r + split, ... : 4 columns per lane, the parts in rank order
+  const int col = n0 + lane * 4;
+  int o = 0;
+  while (o < p.n_outs - 1 && col >= p.outs[o].end) ++o;
+  const bool four = col + 4 <= p.outs[o].end && wide_ok<O, 4>(p.outs[o]);
+  O* const dst = static_cast<O*>(p.outs[o].out) + (col - p.outs[o].begin);
   for (int j = rank + split * warp; j < rows; j += split * (C::kThreads / 32)) {
-    const uint32_t at = smem_u32(part + j * 128 + lane * 4);
+    const uint32_t at = smem_u32(sums + j * C::kPitch + lane * 4);
     float v[4] = {0.f, 0.f, 0.f, 0.f};
     for (int r = 0; r < split; ++r) {
       const float4 f = ld_shared_remote_f4(mapa_shared(at, r));
@@ -472,11 +507,19 @@ __global__ void __launch_bounds__(192) linear_split_kernel(const __grid_constant
       v[2] += f.z;
       v[3] += f.w;
     }
-    const int col = n0 + lane * 4;
-    int o = 0;
-    for (int e = 0; e < 4 && col + e < p.n; ++e) {
-      while (col + e >= p.outs[o].end) ++o;
-      static_cast<O*>(p.outs[o].out)[(row0 + j) * p.outs[o].ld + (col + e - p.outs[o].begin)] = from_f32<O>(v[e]);
+    if (four) {
+      if constexpr (sizeof(O) == 4) {
+        *reinterpret_cast<float4*>(dst + (row0 + j) * p.outs[o].ld) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        __nv_bfloat162 t[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+        *reinterpret_cast<uint2*>(dst + (row0 + j) * p.outs[o].ld) =
+            make_uint2(*reinterpret_cast<uint32_t*>(&t[0]), *reinterpret_cast<uint32_t*>(&t[1]));
+      }
+    } else {   // a destination ends among the four, or its rows are not aligned for them
+      for (int e = 0, oe = o; e < 4 && col + e < p.n; ++e) {
+        while (col + e >= p.outs[oe].end) ++oe;
+        static_cast<O*>(p.outs[oe].out)[(row0 + j) * p.outs[oe].ld + (col + e - p.outs[oe].begin)] = from_f32<O>(v[e]);
+      }
     }
   }
   cluster_sync();                                           // no CTA leaves while its parts are read
@@ -531,6 +574,14 @@ cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   return launch_chained(linear_pair_kernel<O>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, a, maps);
 }
 
+// How many parts of K a cluster takes: as many as the SMs hold at once, each with a block at least.
+template <int NT>
+int split_of(int64_t tiles, int blocks, int sms) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= SplitCfg<NT>::kPerSm * sms && split * 2 <= blocks) split *= 2;
+  return split;
+}
+
 template <int NT, typename O>
 cudaError_t launch_split(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   using C = SplitCfg<NT>;
@@ -544,9 +595,7 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int row_tiles = ceil_div(a.m, NT), blocks = ceil_div(a.k, kFp8Group);
   const int64_t tiles = (int64_t)row_tiles * ceil_div(a.n, 128);
-  // as many parts of K as fill the GPU with two CTAs on every SM, each with a block at least
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * sms && split * 2 <= blocks) split *= 2;
+  const int split = split_of<NT>(tiles, blocks, sms);
   if (tiles * split > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
@@ -565,14 +614,34 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, O>, a, maps, split, row_tiles);
 }
 
+// Whether more than 64 rows are better served by pairs of CTAs.  Both kernels walk their tiles in waves
+// over the SMs; the constants (nanoseconds for a block of K, and for a tile's start and end) are from
+// B200 runs: the estimates are within 15% of the times below, and the choice falls right for all.
+//   rows x columns x K         pairs    split
+//   128 x 25152 x 4096         38 us    37 us
+//   256 x 25152 x 4096         39       55
+//   256 x  4096 x 16384        62       30
+//   1024 x 4096 x 16384        68      100
+//   333 x  1000 x 1960         14        7.5
+//   2048 x  576 x 4096         20       17
+bool pairs_pay(int64_t m, int64_t n, int blocks, int sms) {
+  const int64_t pair_tiles = (int64_t)ceil_div(m, kPairM) * ceil_div(n, kPairN);
+  const int64_t pair_waves = ceil_div(pair_tiles, sms / 2);
+  const int64_t tiles = (int64_t)ceil_div(m, 128) * ceil_div(n, 128);
+  const int split = split_of<128>(tiles, blocks, sms);
+  const int64_t waves = ceil_div(tiles * split, sms);
+  return 4000 + pair_waves * (1500 + (int64_t)blocks * 480) < waves * (5000 + (int64_t)ceil_div(blocks, split) * 380);
+}
+
 template <typename O>
 cudaError_t launch(const Fp8LinearArgs& a, cudaStream_t st) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (a.m > 128) return launch_pair<O>(a, sms, st);
-  if (a.m > 64) return launch_split<128, O>(a, sms, st);
+  if (a.m > 64)
+    return pairs_pay(a.m, a.n, ceil_div(a.k, kFp8Group), sms) ? launch_pair<O>(a, sms, st) : launch_split<128, O>(a, sms, st);
+  // the smallest of 16, 32 and 64 rows that holds them all: every tile reads its weight rows once
   if (a.m > 32) return launch_split<64, O>(a, sms, st);
   if (a.m > 16) return launch_split<32, O>(a, sms, st);
   return launch_split<16, O>(a, sms, st);
