@@ -47,8 +47,10 @@ __device__ __forceinline__ float block_sum(float v) {
 }
 
 // ---------------------------------------------------------------- rows held in registers
-// One CTA per row, and the row read once: every thread keeps its values of h until the sum of squares
-// is known.  Two layouts:
+// One CTA per row (without a norm: per 4096 columns of a row), and the row read once: every thread keeps
+// its values of h until the sum of squares is known, as they are stored, so that in bf16 32 registers
+// suffice and an SM holds all its 2048 threads.  Bound by memory: 16384 x 4096 bf16 with the residual
+// (472 MB) takes 72 us on a B200, 6.57 TB/s; 82 to 90 us with h kept in fp32.  Two layouts:
 //   * pieces of 8 (rows that are 16-byte aligned, d a multiple of 8): thread t holds the pieces t, t + T,
 //     ..., of T threads, so 16 neighbouring lanes hold a block of 128 and its maximum takes 4 exchanges;
 //   * elements (anything else): a warp holds the blocks w, w + W, ..., lane l the elements l + 32 e, so
@@ -56,40 +58,52 @@ __device__ __forceinline__ float block_sum(float v) {
 constexpr int kPiece = 8;
 constexpr int kMaxThreads = 1024;
 
+// 8 consecutive values of type T as they are stored.
 template <typename T>
-__device__ __forceinline__ void load_piece(const T* p, float (&v)[kPiece]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Piece {
+  uint4 u[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    for (int e = 0; e < (int)sizeof(T) / 2; ++e) u[e] = reinterpret_cast<const uint4*>(p)[e];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(T) / 2; ++e) reinterpret_cast<uint4*>(p)[e] = u[e];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(T) / 2; ++e) u[e] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void values(float (&v)[kPiece]) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) v[e] = __uint_as_float(w[e]);
+    } else {
+      const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      }
     }
   }
-}
-
-// Rounds the piece to T, stores it and leaves the rounded values in v.
-template <typename T>
-__device__ __forceinline__ void store_piece(T* p, float (&v)[kPiece]) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    uint32_t w[4];
+  // Rounds to T.
+  __device__ __forceinline__ void set(const float (&v)[kPiece]) {
+    if constexpr (sizeof(T) == 4) {
+      u[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+      u[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-      w[e] = *reinterpret_cast<uint32_t*>(&t);
-      v[2 * e] = __uint_as_float(w[e] << 16);
-      v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+      for (int e = 0; e < 4; ++e) {
+        __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
+        w[e] = *reinterpret_cast<uint32_t*>(&t);
+      }
+      u[0] = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-}
+};
 
 __device__ __forceinline__ uint2 codes_of(const float (&v)[kPiece], float rs) {
   uint32_t h[4];
@@ -112,68 +126,77 @@ __device__ __forceinline__ float half_warp_max(float m) {
   return m;
 }
 
-template <typename T, int PIECES, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_quant_pieces_kernel(NormQuantArgs a) {
+template <typename T, int PIECES, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQuantArgs a, int parts) {
   pdl_trigger();
   pdl_wait();
-  const int64_t i = blockIdx.x;
+  int64_t i = blockIdx.x;
   const int d = a.d, threads = blockDim.x;
+  int j0 = (int)threadIdx.x * kPiece;
+  if (parts > 1) {   // (only without a norm)
+    i = blockIdx.x / parts;
+    j0 += (int)(blockIdx.x % parts) * threads * PIECES * kPiece;
+  }
+  const int step = threads * kPiece;
   const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
-  float h[PIECES][kPiece];
+  Piece<T> h[PIECES];   // as stored: h is rounded to T, so nothing is lost
 #pragma unroll
   for (int c = 0; c < PIECES; ++c) {
-    const int j = ((int)threadIdx.x + c * threads) * kPiece;
-    if (j < d) {
-      load_piece(x + j, h[c]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kPiece; ++e) h[c][e] = 0.f;
-    }
+    if (j0 + c * step < d) h[c].load(x + j0 + c * step);
+    else h[c].zero();
   }
   if (a.residual) {
     const T* r = static_cast<const T*>(a.residual) + i * d;
-    float t[PIECES][kPiece];
+    Piece<T> t[PIECES];
 #pragma unroll
-    for (int c = 0; c < PIECES; ++c) {
-      const int j = ((int)threadIdx.x + c * threads) * kPiece;
-      if (j < d) load_piece(r + j, t[c]);
-    }
+    for (int c = 0; c < PIECES; ++c)
+      if (j0 + c * step < d) t[c].load(r + j0 + c * step);
 #pragma unroll
-    for (int c = 0; c < PIECES; ++c) {
-      const int j = ((int)threadIdx.x + c * threads) * kPiece;
-      if (j < d) {
+    for (int c = 0; c < PIECES; ++c)
+      if (j0 + c * step < d) {
+        float f[kPiece], g[kPiece];
+        h[c].values(f);
+        t[c].values(g);
 #pragma unroll
-        for (int e = 0; e < kPiece; ++e) h[c][e] += t[c][e];
-        store_piece(static_cast<T*>(a.residual_out) + i * d + j, h[c]);
+        for (int e = 0; e < kPiece; ++e) f[e] += g[e];
+        h[c].set(f);
+        h[c].store(static_cast<T*>(a.residual_out) + i * d + j0 + c * step);
       }
-    }
   }
+  float inv = 1.f;
   if (a.gamma) {
     float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < PIECES; ++c)
-#pragma unroll
-      for (int e = 0; e < kPiece; ++e) sum += h[c][e] * h[c][e];
-    const float inv = 1.f / sqrtf(block_sum(sum) / (float)d + a.eps);
-#pragma unroll
     for (int c = 0; c < PIECES; ++c) {
-      const int j = ((int)threadIdx.x + c * threads) * kPiece;
-      if (j < d) {
-        float g[kPiece];
-        load_piece(a.gamma + j, g);
+      float f[kPiece];
+      h[c].values(f);
 #pragma unroll
-        for (int e = 0; e < kPiece; ++e) h[c][e] = h[c][e] * inv * g[e];
-      }
+      for (int e = 0; e < kPiece; ++e) sum += f[e] * f[e];
     }
+    inv = 1.f / sqrtf(block_sum(sum) / (float)d + a.eps);
   }
 #pragma unroll
   for (int c = 0; c < PIECES; ++c) {
-    const int j = ((int)threadIdx.x + c * threads) * kPiece;
-    const float s = scale_of(half_warp_max(piece_max(h[c])));
+    const int j = j0 + c * step;
+    float f[kPiece];
+    h[c].values(f);
+    if (a.gamma && j < d) {
+      Piece<float> g;
+      g.load(a.gamma + j);
+      float gf[kPiece];
+      g.values(gf);
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) f[e] = f[e] * inv * gf[e];
+    }
+    const float s = scale_of(half_warp_max(piece_max(f)));
     if (j < d) {
-      *reinterpret_cast<uint2*>(a.codes + i * a.ld + j) = codes_of(h[c], 1.f / s);
+      *reinterpret_cast<uint2*>(a.codes + i * a.ld + j) = codes_of(f, 1.f / s);
       if (j % kFp8Group == 0) a.scale[j / kFp8Group * a.ld_scale + i] = s;
-      if (a.y) store_piece(static_cast<T*>(a.y) + i * d + j, h[c]);
+      if (a.y) {
+        Piece<T> y;
+        y.set(f);
+        y.store(static_cast<T*>(a.y) + i * d + j);
+      }
     }
   }
 }
@@ -305,61 +328,84 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_long_kernel(NormQuantA
 }
 
 // ---------------------------------------------------------------- weights
-constexpr int kWeightThreads = 256;
+// One CTA per block of 128 x 128, read once.  WIDE: in pieces of 8 (16-byte aligned rows), 16 lanes along a
+// row; else a warp along a row, lane l with the elements l + 32 e.  Every thread keeps what it read, as it
+// was read, until the block's maximum is known.  Bound by memory: several CTAs share an SM so that one
+// block's loads run beside another's stores, and what a thread keeps decides how many.  bf16, 25152 x 4096
+// (309 MB) on a B200: 49 us, 6.3 TB/s, with three CTAs; 58 with two, 59 with four, which spill.
+constexpr int kWeightThreads = 512, kWeightElementThreads = 1024;
 
 // Largest magnitude of the CTA's threads.
+template <int THREADS>
 __device__ __forceinline__ float block_max(float m) {
-  __shared__ float part[kWeightThreads / 32];
+  __shared__ float part[THREADS / 32];
   m = warp_max_nan(m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
+  m = part[threadIdx.x & (THREADS / 32 - 1)];
 #pragma unroll
-  for (int i = 0; i < kWeightThreads / 32; ++i) m = max_nan(m, part[i]);
+  for (int o = THREADS / 64; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
-// One CTA per block of 128 x 128, read once into registers.  WIDE: in pieces of 8 (16-byte aligned rows),
-// 16 threads along a row; else element by element, 128 threads along a row.
-template <typename T, bool WIDE>
-__global__ void __launch_bounds__(kWeightThreads) quant_weight_kernel(QuantWeightArgs a, int k_blocks) {
+template <typename T>
+__global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 2 ? 3 : 2) quant_weight_pieces_kernel(QuantWeightArgs a, int k_blocks) {
   pdl_trigger();
   pdl_wait();
-  const int kb = blockIdx.x % k_blocks;
-  const int64_t row0 = (int64_t)(blockIdx.x / k_blocks) * kFp8Group;
-  const T* w = static_cast<const T*>(a.w);
-  constexpr int W = WIDE ? kPiece : 1, ACROSS = kFp8Group / W, STEP = kWeightThreads / ACROSS, ROWS = kFp8Group / STEP;
-  const int col = kb * kFp8Group + (int)(threadIdx.x % ACROSS) * W;
-  const int64_t row = row0 + threadIdx.x / ACROSS;
-  float v[ROWS][W], m = 0.f;
+  constexpr int STEP = kWeightThreads / 16, ROWS = kFp8Group / STEP;
+  const int col = (int)(blockIdx.x % k_blocks) * kFp8Group + (int)(threadIdx.x & 15) * kPiece;
+  const int64_t row = (int64_t)(blockIdx.x / k_blocks) * kFp8Group + (threadIdx.x >> 4);
+  const T* w = static_cast<const T*>(a.w) + row * a.k + col;
+  Piece<T> v[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     const bool in = row + r * STEP < a.n && col < a.k;
-    if constexpr (WIDE) {
-      if (in) {
-        load_piece(w + (row + r * STEP) * a.k + col, v[r]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < W; ++e) v[r][e] = 0.f;
-      }
-    } else {
-      v[r][0] = in ? to_f32(w[(row + r * STEP) * a.k + col]) : 0.f;
-    }
+    if (in) v[r].load(w + (int64_t)r * STEP * a.k);
+    else v[r].zero();
   }
+  float m = 0.f;
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-    for (int e = 0; e < W; ++e) m = max_nan(m, fabsf(v[r][e]));
-  const float s = scale_of(block_max(m)), rs = 1.f / s;
+  for (int r = 0; r < ROWS; ++r) {
+    float f[kPiece];
+    v[r].values(f);
+    m = max_nan(m, piece_max(f));
+  }
+  const float s = scale_of(block_max<kWeightThreads>(m)), rs = 1.f / s;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     if (row + r * STEP >= a.n || col >= a.k) continue;
-    uint8_t* dst = a.codes + (row + r * STEP) * a.ld + col;
-    if constexpr (WIDE) {
-      *reinterpret_cast<uint2*>(dst) = codes_of(v[r], rs);
-    } else {
-      *dst = code_of(v[r][0] * rs);
-    }
+    float f[kPiece];
+    v[r].values(f);
+    *reinterpret_cast<uint2*>(a.codes + (row + r * STEP) * a.ld + col) = codes_of(f, rs);
   }
+  if (threadIdx.x == 0) a.scale[blockIdx.x] = s;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kWeightElementThreads) quant_weight_elements_kernel(QuantWeightArgs a, int k_blocks) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int STEP = kWeightElementThreads / 32, ROWS = kFp8Group / STEP;
+  const int col = (int)(blockIdx.x % k_blocks) * kFp8Group + (int)(threadIdx.x & 31);
+  const int64_t row = (int64_t)(blockIdx.x / k_blocks) * kFp8Group + (threadIdx.x >> 5);
+  const T* w = static_cast<const T*>(a.w) + row * a.k + col;
+  float v[ROWS][4], m = 0.f;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[r][e] = row + r * STEP < a.n && col + e * 32 < a.k ? to_f32(w[(int64_t)r * STEP * a.k + e * 32]) : 0.f;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = max_nan(m, fabsf(v[r][e]));
+  const float s = scale_of(block_max<kWeightElementThreads>(m)), rs = 1.f / s;
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (row + r * STEP < a.n && col + e * 32 < a.k)
+        a.codes[(row + r * STEP) * a.ld + col + e * 32] = code_of(v[r][e] * rs);
   if (threadIdx.x == 0) a.scale[blockIdx.x] = s;
 }
 
@@ -367,23 +413,38 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 
+// CTAs of 256 threads on an SM that the pieces kernel is compiled for: what a thread keeps of a row fits 32
+// registers in bf16 (all of an SM's threads), 64 in fp32.
+template <typename T>
+constexpr int kCtasOf = sizeof(T) == 2 ? 8 : 4;
+
 template <typename T>
 cudaError_t launch_norm(const NormQuantArgs& a, cudaStream_t st) {
+  constexpr int kCtas = kCtasOf<T>;
   const dim3 grid(a.n);
   const bool wide = a.d % kPiece == 0 && a.ld_x * sizeof(T) % 16 == 0 && on16(a.x) && on16(a.residual) &&
                     on16(a.residual_out) && on16(a.gamma) && on16(a.y);
   const int pieces = (a.d + kPiece - 1) / kPiece, blocks = (a.d + kFp8Group - 1) / kFp8Group;
+  if (wide && !a.gamma) {   // every block of 128 stands alone: rows in parts of up to 4096 columns
+    const int per = (pieces + 1) / 2, threads = per < 256 ? round32(per) : 256;
+    const int parts = (pieces + 2 * threads - 1) / (2 * threads);
+    if ((int64_t)a.n * parts <= INT32_MAX)
+      return launch_chained(norm_quant_pieces_kernel<T, 2, 256, kCtas>, dim3(a.n * parts), dim3(threads), 0, st, a,
+                            parts);
+  }
   if (wide && pieces <= 4 * kMaxThreads) {
-    // few rows: one piece per thread, the shortest chain; many: more loads in flight per thread
+    // few rows: one piece per thread, the shortest chain; many: CTAs of 256 threads with 2 pieces, a full SM's
+    // threads of them
     const bool few = a.n <= 512;
-    if (pieces <= (few ? kMaxThreads : 128))
-      return launch_chained(norm_quant_pieces_kernel<T, 1, kMaxThreads>, grid, dim3(round32(pieces)), 0, st, a);
-    if (pieces <= (few ? 2 * kMaxThreads : 1024))
-      return launch_chained(norm_quant_pieces_kernel<T, 2, kMaxThreads>, grid, dim3(round32((pieces + 1) / 2)), 0, st,
-                            a);
-    const dim3 block(round32((pieces + 3) / 4));
-    return pieces <= 4 * 512 ? launch_chained(norm_quant_pieces_kernel<T, 4, 512>, grid, block, 0, st, a)
-                             : launch_chained(norm_quant_pieces_kernel<T, 4, kMaxThreads>, grid, block, 0, st, a);
+    if (pieces <= (few ? kMaxThreads : 256))
+      return launch_chained(norm_quant_pieces_kernel<T, 1, kMaxThreads, 1>, grid, dim3(round32(pieces)), 0, st, a, 1);
+    if (!few && pieces <= 2 * 256)
+      return launch_chained(norm_quant_pieces_kernel<T, 2, 256, kCtas>, grid, dim3(round32((pieces + 1) / 2)), 0, st, a, 1);
+    if (pieces <= 2 * kMaxThreads)
+      return launch_chained(norm_quant_pieces_kernel<T, 2, kMaxThreads, kCtas / 4>, grid, dim3(round32((pieces + 1) / 2)), 0, st,
+                            a, 1);
+    return launch_chained(norm_quant_pieces_kernel<T, 4, kMaxThreads, 1>, grid, dim3(round32((pieces + 3) / 4)), 0, st,
+                          a, 1);
   }
   if (blocks <= 2 * 32)
     return launch_chained(norm_quant_elements_kernel<T, 2, kMaxThreads>, grid, dim3((blocks + 1) / 2 * 32), 0, st, a);
@@ -397,9 +458,10 @@ cudaError_t launch_weight(const QuantWeightArgs& a, cudaStream_t st) {
   const int k_blocks = (int)(((int64_t)a.k + kFp8Group - 1) / kFp8Group);
   const int64_t ctas = (int64_t)k_blocks * (((int64_t)a.n + kFp8Group - 1) / kFp8Group);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)ctas), block(kWeightThreads);
-  return a.k % kPiece == 0 && on16(a.w) ? launch_chained(quant_weight_kernel<T, true>, grid, block, 0, st, a, k_blocks)
-                                        : launch_chained(quant_weight_kernel<T, false>, grid, block, 0, st, a, k_blocks);
+  const dim3 grid((unsigned)ctas);
+  if (a.k % kPiece == 0 && on16(a.w))
+    return launch_chained(quant_weight_pieces_kernel<T>, grid, dim3(kWeightThreads), 0, st, a, k_blocks);
+  return launch_chained(quant_weight_elements_kernel<T>, grid, dim3(kWeightElementThreads), 0, st, a, k_blocks);
 }
 
 }  // namespace
