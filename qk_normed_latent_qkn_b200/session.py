@@ -9,6 +9,11 @@ weights, the value up-projection (optional), the absorbed queries and a
 decode workspace, and forwards to ``qkn_append``, ``qkn_absorb_query``,
 ``qkn_decode`` and ``qkn_decode_up``.  It moves host
 arrays to the device and nothing else: all arithmetic runs in libqkn.
+
+With ``load_projections`` the session starts from hidden states and ends in
+them: the layer's projections around the attention run in 8 bits
+(``qkn_norm_quant``, ``qkn_fp8_linear``; weights quantised on the device at
+load time, ``qkn_quant_weight``).
 """
 from __future__ import annotations
 
@@ -17,9 +22,9 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (AK_CACHE, KERNEL_AUTO, Cache, Dims, GqaCache, absorb_query, append, append_absorb, decode, decode_up,
-               gqa_append, gqa_decode, gqa_workspace_size, key_gram, decode_workspace_size, read_device_status,
-               workspace_init)
+from . import (AK_CACHE, KERNEL_AUTO, OK, WORKSPACE_BYTES, Cache, Dims, Fp8Rows, Fp8Weight, GqaCache, absorb_query,
+               append, append_absorb, decode, decode_up, decode_workspace_size, fp8_linear, gqa_append, gqa_decode,
+               gqa_workspace_size, key_gram, norm_quant, quant_weight, read_device_status, workspace_init)
 
 
 def to_device(x, dtype: torch.dtype, device) -> torch.Tensor:
@@ -37,6 +42,12 @@ class DecodeSession:
         self.w_uv: Optional[torch.Tensor] = None
         self.q_tilde = self.a_q = self.q_rope_hat = None
         self.workspace: Optional[torch.Tensor] = None
+        self.w_in: Optional[Fp8Weight] = None
+        self.w_out: Optional[Fp8Weight] = None
+        self.gamma_x: Optional[torch.Tensor] = None
+        self.x8 = self.o8 = None                       # the projections' inputs in 8 bits
+        self.q = self.q_rope = self.c_new = self.k_rope_new = None
+        self.proj_workspace: Optional[torch.Tensor] = None
 
     # ------------------------------------------------------------ weights
     def load_weights(self, w_k, gamma_q, gamma_k, gamma_qr, gamma_kr) -> None:
@@ -53,6 +64,74 @@ class DecodeSession:
     def load_value_weights(self, w_uv) -> None:
         """W^UV [H, r_kv, d_v], kept in the storage dtype (the fused merge reads it every step)."""
         self.w_uv = to_device(w_uv, self.dims.torch_dtype, self.device)
+
+    def load_projections(self, gamma_x, w_in, w_out=None) -> None:
+        """The layer's projections, quantised to 8 bits here (in the storage dtype until then): ``gamma_x`` [D] the
+        norm in front of them, ``w_in`` [H d_h + H d_R + r + d_R, D] with the rows of q, q^R, c and k^R in this order,
+        ``w_out`` [D, H d_v] the output projection of the up-projected values (needs load_value_weights)."""
+        d, dev = self.dims, self.device
+        self.gamma_x = to_device(gamma_x, torch.float32, dev)
+        self.w_in = self._quantised(w_in)
+        if self.w_in.rows != sum(self.projection_widths()) or self.w_in.cols != self.gamma_x.shape[0]:
+            raise ValueError("w_in is [H d_h + H d_R + r + d_R, D], gamma_x [D]")
+        self.w_out = None
+        if w_out is not None:
+            self.w_out = self._quantised(w_out)
+            if self.w_uv is None or self.w_out.cols != d.num_heads * self.w_uv.shape[-1]:
+                raise ValueError("w_out is [D, H d_v] for the value weights loaded before")
+        self.proj_workspace = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+        workspace_init(self.proj_workspace)
+
+    def _quantised(self, w) -> Fp8Weight:
+        w = to_device(w, self.dims.torch_dtype, self.device)
+        q = Fp8Weight.empty(int(w.shape[0]), int(w.shape[1]), self.device)
+        quant_weight(w, q)
+        return q
+
+    def projection_widths(self):
+        """Columns of q, q^R, c and k^R in the input projection."""
+        d = self.dims
+        return d.num_heads * d.d_h, d.num_heads * d.d_rope, d.r_kv, d.d_rope
+
+    # ------------------------------------------------------------ hidden states
+    def project(self, x, residual=None):
+        """Hidden states [n, D] -> q [n, H, d_h], q^R [n, H, d_R], c [n, r], k^R [n, d_R] (raw, as append and absorb
+        take them).  ``residual`` (a device tensor [n, D]) is added first and takes the sum.  The output buffers are
+        reused while n stays the same."""
+        d, dt, dev = self.dims, self.dims.torch_dtype, self.device
+        if self.w_in is None:
+            raise RuntimeError("project needs load_projections first")
+        x = to_device(x, dt, dev)
+        n = int(x.shape[0])
+        if self.q is None or self.q.shape[0] != n:
+            self.x8 = Fp8Rows.empty(n, self.w_in.cols, dev)
+            self.q, self.q_rope, self.c_new, self.k_rope_new = (
+                torch.empty((n, w), dtype=dt, device=dev) for w in self.projection_widths())
+        norm_quant(x, self.x8, gamma=self.gamma_x, eps=d.eps, residual=residual, residual_out=residual)
+        fp8_linear(self.x8, self.w_in, (self.q, self.q_rope, self.c_new, self.k_rope_new), self.proj_workspace)
+        return (self.q.view(n, d.num_heads, d.d_h), self.q_rope.view(n, d.num_heads, d.d_rope), self.c_new,
+                self.k_rope_new)
+
+    def prepare_hidden(self, x, slot, pos, residual=None) -> None:
+        """A decode step's preparation from hidden states: every row of ``x`` is a new token and a query at its
+        position (append, query absorption)."""
+        q, q_rope, c, k_rope = self.project(x, residual)
+        pos = to_device(pos, torch.int32, self.device)
+        self.prepare(c, k_rope, slot, pos, q, q_rope, pos)
+
+    def project_out(self, o_v, out=None):
+        """The output projection: o_v [..., H, d_v] -> hidden states [n, D]."""
+        if self.w_out is None:
+            raise RuntimeError("project_out needs load_projections with w_out first")
+        rows = o_v.reshape(-1, self.w_out.cols)
+        n = int(rows.shape[0])
+        if self.o8 is None or self.o8.rows != n:
+            self.o8 = Fp8Rows.empty(n, self.w_out.cols, self.device)
+        if out is None:
+            out = torch.empty((n, self.w_out.rows), dtype=self.dims.torch_dtype, device=self.device)
+        norm_quant(rows, self.o8)
+        fp8_linear(self.o8, self.w_out, (out,), self.proj_workspace)
+        return out
 
     # ------------------------------------------------------------ cache
     def append(self, c, k_rope_raw, slot, pos, chunk: int = 1 << 16) -> None:
@@ -142,10 +221,17 @@ class DecodeSession:
         return out_v, lse
 
     def device_status(self) -> int:
-        return read_device_status(self.workspace)
+        """The first error that a kernel recorded: the decode's, then the projections'."""
+        status = read_device_status(self.workspace) if self.workspace is not None or self.proj_workspace is None else OK
+        if status == OK and self.proj_workspace is not None:
+            status = read_device_status(self.proj_workspace)
+        return status
 
     def clear_status(self) -> None:
-        workspace_init(self.workspace)
+        if self.workspace is not None or self.proj_workspace is None:
+            workspace_init(self.workspace)
+        if self.proj_workspace is not None:
+            workspace_init(self.proj_workspace)
 
 
 def session_from_inputs(inp, device="cuda", dtype=None) -> DecodeSession:

@@ -14,12 +14,17 @@ Usage::
     step = DecodeStep(session, batch=B, s_q=1, max_blocks=M, n_tok=B)
     step.host_in["c"][:] = ...        # fill the pinned inputs (see NAMES)
     out, lse = step.run()             # pinned host outputs, valid after run() returns
+
+``LayerStep`` is the same for a whole attention layer, hidden states in and
+out: norm with the residual's addition, input projections, append + absorb,
+decode with the value up-projection, output projection (the projections in 8
+bits, see DecodeSession.load_projections).
 """
 from __future__ import annotations
 
 import torch
 
-from . import AK_CACHE, KERNEL_AUTO, append_absorb, decode
+from . import AK_CACHE, KERNEL_AUTO, Fp8Rows, append_absorb, decode, decode_up, fp8_linear, norm_quant
 
 
 class DecodeStep:
@@ -109,3 +114,71 @@ class DecodeStep:
         self.graph.replay()
         torch.cuda.current_stream(self.session.device).synchronize()
         return self.host_out
+
+
+class LayerStep(DecodeStep):
+    """One attention layer's decode step: row b s_q + j of ``x`` and ``residual`` is the j-th new token of sequence b.
+    ``run`` returns pinned (hidden, residual): the layer's output [n, D] and x + residual, which the next layer adds."""
+
+    NAMES = ("x", "residual", "slot", "pos", "block_table", "seq_lens")
+
+    def __init__(self, session, batch: int, s_q: int, max_blocks: int, kernel: int = KERNEL_AUTO,
+                 ak_mode: int = AK_CACHE, head_tile: int = 0):
+        if session.w_in is None or session.w_out is None:
+            raise RuntimeError("LayerStep needs a session with load_projections (w_out included)")
+        d = session.dims
+        dt, dev, i32 = d.torch_dtype, session.device, torch.int32
+        n, width = batch * s_q, session.w_in.cols
+        self.session, self.batch, self.s_q, self.kernel, self.ak_mode = session, batch, s_q, kernel, ak_mode
+        self.head_tile = head_tile
+        shapes = {
+            "x": ((n, width), dt), "residual": ((n, width), dt), "slot": ((n,), i32), "pos": ((n,), i32),
+            "block_table": ((batch, max_blocks), i32), "seq_lens": ((batch,), i32),
+        }
+        in_off, in_bytes = self._layout([shapes[k] for k in self.NAMES])
+        self._host_in_buf = torch.zeros(in_bytes, dtype=torch.uint8, pin_memory=True)
+        self._dev_in_buf = torch.zeros(in_bytes, dtype=torch.uint8, device=dev)
+        self.host_in = self._views(self._host_in_buf, self.NAMES, shapes, in_off)
+        self.dev_in = self._views(self._dev_in_buf, self.NAMES, shapes, in_off)
+        oshapes = {"hidden": ((n, session.w_out.rows), dt), "residual": ((n, width), dt)}
+        out_off, out_bytes = self._layout([oshapes["hidden"], oshapes["residual"]])
+        self._host_out_buf = torch.zeros(out_bytes, dtype=torch.uint8, pin_memory=True)
+        self._dev_out_buf = torch.zeros(out_bytes, dtype=torch.uint8, device=dev)
+        dv = self._views(self._dev_out_buf, ("hidden", "residual"), oshapes, out_off)
+        hv = self._views(self._host_out_buf, ("hidden", "residual"), oshapes, out_off)
+        self.hidden, self.residual = dv["hidden"], dv["residual"]
+        self.host_out = (hv["hidden"], hv["residual"])
+        # buffers of its own, so that other sizes on the same session leave the captured ones alone, and the
+        # weights that the graph will read, so that they live as long as it does
+        self.gamma_x, self.w_in, self.w_out, self.w_uv = session.gamma_x, session.w_in, session.w_out, session.w_uv
+        self.proj_workspace = session.proj_workspace
+        self.x8 = Fp8Rows.empty(n, width, dev)
+        self.o8 = Fp8Rows.empty(n, session.w_out.cols, dev)
+        self.q, self.q_rope, self.c, self.k_rope = (torch.empty((n, w), dtype=dt, device=dev)
+                                                    for w in session.projection_widths())
+        self.q_tilde = torch.empty((n, d.num_heads, d.r_kv), dtype=dt, device=dev)
+        self.a_q = torch.empty((n, d.num_heads), dtype=torch.float32, device=dev)
+        self.q_rope_hat = torch.empty((n, d.num_heads, d.d_rope), dtype=dt, device=dev)
+        self.o_v = torch.empty((n, session.w_out.cols), dtype=dt, device=dev)
+        self.lse = torch.empty((n, d.num_heads), dtype=torch.float32, device=dev)
+        self.workspace = session.ensure_workspace(batch, s_q)
+        # the decode may start beside the preparation only where that is one launch
+        self.step_writes_only = 0 < n <= 256 and session.cache.ak_scratch is not None
+        self.graph = None
+        self.h2d_bytes = in_bytes
+        self.d2h_bytes = out_bytes
+
+    def _body(self) -> None:
+        s, d, di = self.session, self.session.dims, self.dev_in
+        self._dev_in_buf.copy_(self._host_in_buf, non_blocking=True)
+        norm_quant(di["x"], self.x8, gamma=self.gamma_x, eps=d.eps, residual=di["residual"], residual_out=self.residual)
+        fp8_linear(self.x8, self.w_in, (self.q, self.q_rope, self.c, self.k_rope), self.proj_workspace)
+        append_absorb(d, s.cache, self.c, self.k_rope, di["slot"], di["pos"], self.q, self.q_rope, di["pos"], s.w_k,
+                      s.key_gram, s.gamma_q, s.gamma_k, s.gamma_qr, s.gamma_kr, self.q_tilde, self.a_q,
+                      self.q_rope_hat)
+        decode_up(d, s.cache, self.q_tilde, self.a_q, self.q_rope_hat, di["block_table"], di["seq_lens"], self.s_q,
+                  self.w_uv, self.workspace, self.o_v, self.lse, ak_mode=self.ak_mode, kernel=self.kernel,
+                  head_tile=self.head_tile, step_writes_only=self.step_writes_only)
+        norm_quant(self.o_v, self.o8)
+        fp8_linear(self.o8, self.w_out, (self.hidden,), self.proj_workspace)
+        self._host_out_buf.copy_(self._dev_out_buf, non_blocking=True)

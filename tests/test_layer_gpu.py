@@ -1,0 +1,135 @@
+"""An attention layer from hidden states to hidden states, its projections in 8 bits (GPU): the session's calls
+one after the other, and LayerStep's captured graph.  Every stage is compared with its definition in 64 bits on
+the values that the stage before it left on the device, under that stage's own tolerances."""
+import copy
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import qk_normed_latent_qkn_b200 as qkn
+from gpu_common import REL_TOL
+from qk_normed_latent_qkn_b200.session import session_from_inputs
+from qk_normed_latent_qkn_b200.step import LayerStep
+from qkn_inputs import WORKLOADS, make_inputs
+from test_projection_gpu import check_codes, check_product, host
+
+pytestmark = pytest.mark.gpu
+
+CASES = {
+    # fp32 storage, a hidden width that no block of 128 divides
+    "tiny_f32": (WORKLOADS["tiny_f32"].with_(batch=3, context=(100, 300), seed=81), 200),
+    "small_mla_bf16": (WORKLOADS["small_mla_bf16"].with_(batch=4, context=(300, 700), seed=82), 1024),
+    # two new tokens per sequence, four groups
+    "grouped_mtp_bf16": (WORKLOADS["grouped_mtp_bf16"].with_(batch=5, context=(130, 900), seed=83), 1536),
+    # a chunk of a prompt: more rows than the single-launch preparation takes
+    "prefill_mla_bf16": (WORKLOADS["prefill_mla_bf16"].with_(batch=2, s_q=150, context=(150, 400), seed=84), 512),
+}
+
+
+def build(name):
+    wl, width = CASES[name]
+    inp = make_inputs(wl)
+    s = session_from_inputs(inp)
+    n, heads = wl.batch * wl.s_q, wl.heads
+    g = torch.Generator().manual_seed(wl.seed)
+    dt = s.dims.torch_dtype
+    rows = sum(s.projection_widths())
+    x = torch.randn((n, width), generator=g).to(dt).cuda()
+    res = (2 * torch.randn((n, width), generator=g)).to(dt).cuda()
+    gamma = 1 + 0.1 * torch.randn(width, generator=g)
+    w_in = torch.randn((rows, width), generator=g) / width ** 0.5
+    w_out = torch.randn((width, heads * wl.d_v), generator=g) / (heads * wl.d_v) ** 0.5
+    s.load_projections(gamma, w_in, w_out)
+    last = np.concatenate([np.arange(inp.tok_off[b + 1] - wl.s_q, inp.tok_off[b + 1]) for b in range(wl.batch)])
+    return inp, s, x, res, host(gamma), last
+
+
+def check_linear(rows, weight, outs, dtype):
+    av = oracle.row_values(host(rows.codes[:, :rows.cols]), host(rows.scale[:, :rows.rows]))
+    wv = oracle.weight_values(host(weight.codes[:, :weight.cols]), host(weight.scale))
+    got = np.concatenate([host(o).reshape(rows.rows, -1) for o in outs], axis=1)
+    check_product(got, av @ wv.T, np.abs(av) @ np.abs(wv).T, rows.cols, dtype)
+
+
+def check_stages(inp, s, last, x8, h, gamma, parts, o_v, o8, hidden):
+    """x8 from h, the four parts from x8, o_v from the parts over the cache, o8 from o_v, hidden from o8."""
+    wl, dt = inp.wl, s.dims.torch_dtype
+    n = x8.rows
+    check_codes(host(x8.codes[:, :x8.cols]), host(x8.scale[:, :n]), oracle.rms_norm(h, gamma, wl.eps), x8.cols)
+    check_linear(x8, s.w_in, parts, dt)
+    q, q_rope, c, k_rope = (host(t) for t in parts)
+    inp2 = copy.copy(inp)
+    inp2.c, inp2.k_rope = inp.c.copy(), inp.k_rope.copy()
+    inp2.c[last], inp2.k_rope[last] = c, k_rope
+    inp2.q = q.reshape(wl.batch, wl.s_q, wl.heads, wl.d_h)
+    inp2.q_rope = q_rope.reshape(wl.batch, wl.s_q, wl.heads, wl.d_rope)
+    ref = oracle.up_project(oracle.decode(inp2)[0], inp.w_uv).reshape(n, -1)
+    o = host(o_v).reshape(n, -1)
+    assert np.abs(o - ref).max() <= REL_TOL[wl.dtype] * np.abs(ref).max()
+    check_codes(host(o8.codes[:, :o8.cols]), host(o8.scale[:, :n]), o, 0)
+    check_linear(o8, s.w_out, [hidden], dt)
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_session_runs_a_layer_from_hidden_states(name):
+    inp, s, x, res, gamma, last = build(name)
+    total = host(x) + host(res)
+    s.prepare_hidden(x, inp.token_slots()[last], inp.token_positions()[last], residual=res)
+    h = host(res)                                     # the residual took the sum
+    assert np.all(np.abs(h - total) <= np.abs(total) * 2.0 ** -8 + 1e-30)
+    o_v, _ = s.decode_up(inp.block_table, inp.seq_lens, inp.wl.s_q)
+    hidden = s.project_out(o_v)
+    torch.cuda.synchronize()
+    assert s.device_status() == qkn.OK
+    check_stages(inp, s, last, s.x8, h, gamma, (s.q, s.q_rope, s.c_new, s.k_rope_new), o_v, s.o8, hidden)
+
+
+@pytest.mark.parametrize("name", sorted(CASES))
+def test_layer_step_replays_on_new_inputs(name):
+    inp, s, x, res, gamma, last = build(name)
+    wl = inp.wl
+    step = LayerStep(s, wl.batch, wl.s_q, inp.block_table.shape[1])
+    fixed = {"slot": inp.token_slots()[last], "pos": inp.token_positions()[last], "block_table": inp.block_table,
+             "seq_lens": inp.seq_lens}
+    for k, v in fixed.items():
+        step.host_in[k].copy_(torch.from_numpy(np.ascontiguousarray(v)))
+    for a, r in ((res, x), (x, res)):                 # the second replay must not see the first one's values
+        step.host_in["x"].copy_(a)
+        step.host_in["residual"].copy_(r)
+        hidden, total = step.run()
+    assert s.device_status() == qkn.OK
+    check_stages(inp, s, last, step.x8, host(total), gamma, (step.q, step.q_rope, step.c, step.k_rope), step.o_v,
+                 step.o8, hidden)
+    assert torch.equal(total, step.residual.cpu())
+    # other sizes on the same session leave the captured buffers alone
+    first = hidden.clone()
+    s.project(x[:1])
+    step.host_in["x"].copy_(x)
+    again, _ = step.run()
+    # (the key statistics of re-appended tokens are summed with atomics: equal up to rounding and the codes it moves)
+    assert (again.float() - first.float()).abs().max() <= 2 ** -4 * first.float().abs().max()
+
+
+def test_layer_calls_need_their_weights():
+    inp = make_inputs(WORKLOADS["tiny_f32"])
+    s = session_from_inputs(inp)
+    with pytest.raises(RuntimeError):
+        s.project(torch.zeros((1, 64)))
+    with pytest.raises(RuntimeError):
+        LayerStep(s, 1, 1, 4)
+    rows = sum(s.projection_widths())
+    with pytest.raises(ValueError):
+        s.load_projections(torch.ones(64), torch.zeros((rows + 1, 64)))
+    with pytest.raises(ValueError):
+        s.load_projections(torch.ones(63), torch.zeros((rows, 64)))
+    with pytest.raises(ValueError):
+        s.load_projections(torch.ones(64), torch.zeros((rows, 64)), torch.zeros((64, 100)))
+    s.load_projections(torch.ones(64), torch.zeros((rows, 64)))
+    with pytest.raises(RuntimeError):
+        s.project_out(torch.zeros((1, 4, 32), device="cuda"))
+    with pytest.raises(RuntimeError):
+        LayerStep(s, 1, 1, 4)
+    s.project(torch.ones((2, 64)))
+    assert (s.q == 0).all() and s.device_status() == qkn.OK
