@@ -15,6 +15,7 @@
 //     joins through distributed shared memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -208,8 +209,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     RingPos<2> acc;
     for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs)
       for (int b = 0; b < blocks; ++b) {
-        if (!mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles) ||
-            !mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles)) {
+        if (!mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles) ||
+            !mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles)) {
           ok = false;
           break;
         }
@@ -303,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 template <int NT>
 struct SplitCfg {
   static constexpr bool kRows = NT == 128;                               // the rows take the tensor core's M
-  static constexpr int kWarps = NT == 128 ? 8 : 4;                        // epilogue warps, each 32 lanes x
+  static constexpr int kWarps = NT == 16 ? 4 : 8;                         // epilogue warps, each 32 lanes x
   static constexpr int kPart = NT * 4 / kWarps;                          // kPart columns of the accumulator
   static constexpr int kPitch = kRows ? 132 : 128;                       // floats of a row of partial sums
   static constexpr int kThreads = 64 + 32 * kWarps;                       // (and the producer, the MMA)
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
           if constexpr (C::kRows) {
             f[e] = f[e + 1] = f[e + 2] = f[e + 3] = row_f;
           } else {
-            const float4 q = reinterpret_cast<const float4*>(sa)[(c + e) >> 2];
+            const float4 q = reinterpret_cast<const float4*>(sa)[(part * C::kPart + c + e) >> 2];
             f[e] = q.x * s, f[e + 1] = q.y * s, f[e + 2] = q.z * s, f[e + 3] = q.w * s;
           }
         }
@@ -574,28 +575,66 @@ cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   return launch_chained(linear_pair_kernel<O>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, a, maps);
 }
 
+// CTAs of a split kernel that the device holds at once in clusters of `split` (1, 2, 4 or 8): fewer than its
+// SMs' worth (148 SMs: 148, 132 and 120 in clusters of 2, 4 and 8), because a cluster stays within a group of
+// SMs; one cluster too many costs a whole wave (32 x 9472 x 4096: 17.8 us in 74 clusters of 4, 11.1 in 74
+// pairs).  The runtime counts one CTA of a kernel with tensor memory per SM; kPerSm of them do run there.
+// Asked once per device.
+template <int NT, typename O>
+int resident_of(int split, int dev, int sms) {
+  static std::atomic<int> known[64][4];
+  const int at = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+  std::atomic<int>* slot = dev >= 0 && dev < 64 ? &known[dev][at] : nullptr;
+  int n = slot ? slot->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(split * sms);
+  cfg.blockDim = dim3(SplitCfg<NT>::kThreads);
+  cfg.dynamicSmemBytes = SplitCfg<NT>::kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, linear_split_kernel<NT, O>, &cfg) != cudaSuccess || clusters < 1) {
+    (void)cudaGetLastError();
+    clusters = 1;
+  }
+  n = clusters * split * SplitCfg<NT>::kPerSm;
+  if (slot) slot->store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // How many parts of K a cluster takes: as many as the SMs hold at once, each with a block at least.
-template <int NT>
-int split_of(int64_t tiles, int blocks, int sms) {
+template <int NT, typename O>
+int split_of(int64_t tiles, int blocks, int dev, int sms) {
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= SplitCfg<NT>::kPerSm * sms && split * 2 <= blocks) split *= 2;
+  while (split < 8 && split * 2 <= blocks && tiles * split * 2 <= resident_of<NT, O>(split * 2, dev, sms)) split *= 2;
   return split;
 }
 
 template <int NT, typename O>
-cudaError_t launch_split(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
+cudaError_t split_attrs() {
+  static PerDeviceOnce attrs;
+  return once_per_device(attrs, [] { return set_smem_attrs(linear_split_kernel<NT, O>, SplitCfg<NT>::kSmem); });
+}
+
+template <int NT, typename O>
+cudaError_t launch_split(const Fp8LinearArgs& a, int dev, int sms, cudaStream_t st) {
   using C = SplitCfg<NT>;
   LinearMaps maps;
   if (!codes_map(&maps.a, a.a, a.k, a.m, a.lda, NT) || !codes_map(&maps.w, a.w, a.k, a.n, a.ldw, 128) ||
       !make_map(&maps.a_scale, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, a.a_scale, a.m, ceil_div(a.k, kFp8Group), a.ld_as * 4,
                 NT, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  static PerDeviceOnce attrs;
-  cudaError_t e = once_per_device(attrs, [] { return set_smem_attrs(linear_split_kernel<NT, O>, C::kSmem); });
+  const cudaError_t e = split_attrs<NT, O>();
   if (e != cudaSuccess) return e;
   const int row_tiles = ceil_div(a.m, NT), blocks = ceil_div(a.k, kFp8Group);
   const int64_t tiles = (int64_t)row_tiles * ceil_div(a.n, 128);
-  const int split = split_of<NT>(tiles, blocks, sms);
+  const int split = split_of<NT, O>(tiles, blocks, dev, sms);
   if (tiles * split > INT32_MAX) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * split));
@@ -624,11 +663,12 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
 //   1024 x 4096 x 16384        68      100
 //   333 x  1000 x 1960         14        7.5
 //   2048 x  576 x 4096         20       17
-bool pairs_pay(int64_t m, int64_t n, int blocks, int sms) {
+template <typename O>
+bool pairs_pay(int64_t m, int64_t n, int blocks, int dev, int sms) {
   const int64_t pair_tiles = (int64_t)ceil_div(m, kPairM) * ceil_div(n, kPairN);
   const int64_t pair_waves = ceil_div(pair_tiles, sms / 2);
   const int64_t tiles = (int64_t)ceil_div(m, 128) * ceil_div(n, 128);
-  const int split = split_of<128>(tiles, blocks, sms);
+  const int split = split_of<128, O>(tiles, blocks, dev, sms);
   const int64_t waves = ceil_div(tiles * split, sms);
   return 4000 + pair_waves * (1500 + (int64_t)blocks * 480) < waves * (5000 + (int64_t)ceil_div(blocks, split) * 380);
 }
@@ -639,12 +679,15 @@ cudaError_t launch(const Fp8LinearArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (a.m > 64)
-    return pairs_pay(a.m, a.n, ceil_div(a.k, kFp8Group), sms) ? launch_pair<O>(a, sms, st) : launch_split<128, O>(a, sms, st);
+  if (a.m > 64) {
+    if ((e = split_attrs<128, O>()) != cudaSuccess) return e;   // (the estimate asks for the kernel's occupancy)
+    return pairs_pay<O>(a.m, a.n, ceil_div(a.k, kFp8Group), dev, sms) ? launch_pair<O>(a, sms, st)
+                                                                      : launch_split<128, O>(a, dev, sms, st);
+  }
   // the smallest of 16, 32 and 64 rows that holds them all: every tile reads its weight rows once
-  if (a.m > 32) return launch_split<64, O>(a, sms, st);
-  if (a.m > 16) return launch_split<32, O>(a, sms, st);
-  return launch_split<16, O>(a, sms, st);
+  if (a.m > 32) return launch_split<64, O>(a, dev, sms, st);
+  if (a.m > 16) return launch_split<32, O>(a, dev, sms, st);
+  return launch_split<16, O>(a, dev, sms, st);
 }
 
 }  // namespace
