@@ -575,35 +575,42 @@ cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   return launch_chained(linear_pair_kernel<O>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, a, maps);
 }
 
-// CTAs of a split kernel that the device holds at once in clusters of `split` (1, 2, 4 or 8): fewer than its
-// SMs' worth (148 SMs: 148, 132 and 120 in clusters of 2, 4 and 8), because a cluster stays within a group of
-// SMs; one cluster too many costs a whole wave (32 x 9472 x 4096: 17.8 us in 74 clusters of 4, 11.1 in 74
-// pairs).  The runtime counts one CTA of a kernel with tensor memory per SM; kPerSm of them do run there.
-// Asked once per device.
+// Clusters of `size` CTAs that the device holds at once, one CTA per SM: fewer than its SMs' worth, because a
+// cluster stays within a group of SMs (148 SMs: 148, 148, 132 and 120 CTAs in clusters of 1, 2, 4 and 8).
 template <int NT, typename O>
-int resident_of(int split, int dev, int sms) {
-  static std::atomic<int> known[64][4];
-  const int at = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
-  std::atomic<int>* slot = dev >= 0 && dev < 64 ? &known[dev][at] : nullptr;
-  int n = slot ? slot->load(std::memory_order_relaxed) : 0;
-  if (n > 0) return n;
+int clusters_of(int size, int sms) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(split * sms);
+  cfg.gridDim = dim3(size * sms);
   cfg.blockDim = dim3(SplitCfg<NT>::kThreads);
   cfg.dynamicSmemBytes = SplitCfg<NT>::kSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.x = size;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int clusters = 0;
-  if (cudaOccupancyMaxActiveClusters(&clusters, linear_split_kernel<NT, O>, &cfg) != cudaSuccess || clusters < 1) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<NT, O>, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
-    clusters = 1;
+    n = 1;
   }
-  n = clusters * split * SplitCfg<NT>::kPerSm;
+  return n;
+}
+
+// CTAs of a split kernel that the device holds at once in clusters of `split` (2, 4 or 8); a cluster too many
+// costs a whole wave (32 x 9472 x 4096: 17.8 us in 74 clusters of 4, 11.1 in 74 of 2).  The runtime counts one
+// CTA of a kernel with tensor memory per SM.  Where two run there, a cluster needs split / 2 SMs at best and
+// split at worst: the mean of the two counts (280 and 252 for 4 and 8; B200 runs took 272 but not 288, and 264
+// but not 280).  Asked once per device.
+template <int NT, typename O>
+int resident_of(int split, int dev, int sms) {
+  static std::atomic<int> known[64][3];
+  std::atomic<int>* slot = dev >= 0 && dev < 64 ? &known[dev][split / 4] : nullptr;
+  int n = slot ? slot->load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  n = clusters_of<NT, O>(split, sms) * split;
+  if (SplitCfg<NT>::kPerSm == 2) n = (2 * n + clusters_of<NT, O>(split / 2, sms) * split) / 2;
   if (slot) slot->store(n, std::memory_order_relaxed);
   return n;
 }
