@@ -601,8 +601,8 @@ int clusters_of(int size, int sms) {
 // CTAs of a split kernel that the device holds at once in clusters of `split` (2, 4 or 8); a cluster too many
 // costs a whole wave (32 x 9472 x 4096: 17.8 us in 74 clusters of 4, 11.1 in 74 of 2).  The runtime counts one
 // CTA of a kernel with tensor memory per SM.  Where two run there, a cluster needs split / 2 SMs at best and
-// split at worst: the mean of the two counts (280 and 252 for 4 and 8; B200 runs took 272 but not 288, and 264
-// but not 280).  Asked once per device.
+// split at worst: two thirds of the way between the two counts (285 and 256 CTAs for 4 and 8; B200 runs took 272
+// but not 288, and 264 but not 280, without another wave).  Asked once per device.
 template <int NT, typename O>
 int resident_of(int split, int dev, int sms) {
   static std::atomic<int> known[64][3];
@@ -610,7 +610,7 @@ int resident_of(int split, int dev, int sms) {
   int n = slot ? slot->load(std::memory_order_relaxed) : 0;
   if (n > 0) return n;
   n = clusters_of<NT, O>(split, sms) * split;
-  if (SplitCfg<NT>::kPerSm == 2) n = (2 * n + clusters_of<NT, O>(split / 2, sms) * split) / 2;
+  if (SplitCfg<NT>::kPerSm == 2) n = (2 * n + 2 * clusters_of<NT, O>(split / 2, sms) * split) / 3;
   if (slot) slot->store(n, std::memory_order_relaxed);
   return n;
 }
