@@ -119,6 +119,7 @@ constexpr int kLoadCols = 16;                   // columns of one TMEM load
 struct PairBars {
   uint64_t full[kPairStages], empty[kPairStages];
   uint64_t t_full[2], t_empty[2];
+  uint64_t drained;                             // used once a wait has run out: the MMAs in flight are done
   uint32_t tmem;
 };
 constexpr int kPairBoxOff = kPairStages * kPairStageBytes;
@@ -158,6 +159,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(smem_u32(&bars.t_full[i]), 1);
       mbar_init(smem_u32(&bars.t_empty[i]), 2 * kPairWarps);   // of both CTAs
     }
+    mbar_init(smem_u32(&bars.drained), 1);
     mbar_fence_init();
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.w);
@@ -197,9 +199,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ring.next();
       }
     }
-    // the last uses of the stages end before this CTA does: their commits arrive here
+    // the last uses of the stages end before this CTA does: their commits arrive here (after a wait that ran
+    // out, what this pair's copies still bring; the even CTA waits, the odd one for it)
     for (int i = 0; i < kPairStages; ++i) {
       if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
+      if (!ok && rank == 0) (void)mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase ^ 1u, kWaitCycles);
       ring.next();
     }
   } else if (warp == 1 && rank == 0) {
@@ -225,6 +229,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ring.next();
         acc.next();
       }
+    if (!ok) {
+      mma_commit_group2_elect(smem_u32(&bars.drained), 1);
+      (void)mbar_wait_warp(smem_u32(&bars.drained), 0, kWaitCycles);
+    }
   } else if (warp >= 2) {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* box = smem + kPairBoxOff + (warp - 2) * kBoxBytes;
@@ -332,6 +340,7 @@ template <int S, int A>
 struct SplitBars {
   uint64_t full[S], empty[S];
   uint64_t t_full[A], t_empty[A];
+  uint64_t drained;   // as in PairBars
   uint32_t tmem;
 };
 
@@ -364,6 +373,7 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
       mbar_init(smem_u32(&bars.t_full[i]), 2);             // the MMA warp, and its MMAs when they are done
       mbar_init(smem_u32(&bars.t_empty[i]), C::kWarps);
     }
+    mbar_init(smem_u32(&bars.drained), 1);
     mbar_fence_init();
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.w);
@@ -398,6 +408,7 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
     }
     for (int i = 0; i < C::kStages; ++i) {                  // nothing of this CTA's is in flight after this
       if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
+      if (!ok) (void)mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase ^ 1u, kWaitCycles);
       ring.next();
     }
   } else if (warp == 1) {
@@ -422,6 +433,10 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
       mbar_arrive_elect(smem_u32(&bars.t_full[acc.slot]));   // passes on the scales, which came with the stage
       ring.next();
       acc.next();
+    }
+    if (!ok) {
+      mma_commit_elect(smem_u32(&bars.drained));
+      (void)mbar_wait_warp(smem_u32(&bars.drained), 0, kWaitCycles);
     }
   } else {
     const int quad = warp & 3, part = (warp - 2) >> 2;

@@ -10,6 +10,10 @@ Tolerances, from the roundings alone (u = 2^-24, half a step of fp32):
     magnitudes, every block's entry into the total u: (2 * 128 + blocks + 4) u sum|a||w|, and half a step
     of bf16 (2^-8) of the result.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -294,3 +298,92 @@ def test_norm_and_product_captured_replayed_and_on_two_streams(m, n, k):
     for (st, p), o in zip(pairs, want):
         assert torch.equal(p[2], o)
     assert qkn.read_device_status(ws) == qkn.OK
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """What the library sets up once per kernel and device happens inside a capture too."""
+    code = """
+import torch
+import qk_normed_latent_qkn_b200 as qkn
+torch.manual_seed(0)
+ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+w = qkn.Fp8Weight(torch.randn((576, 1024), device="cuda").to(torch.float8_e4m3fn), torch.rand((5, 8), device="cuda"), 1024)
+jobs = []
+for m in (1, 20, 50, 100, 600, 9000):
+    x, q = torch.randn((m, 1024), device="cuda"), qkn.Fp8Rows.empty(m, 1024)
+    jobs.append((x, q, torch.zeros((m, 576), device="cuda")))
+def run():
+    for x, q, out in jobs:
+        qkn.norm_quant(x, q)
+        qkn.fp8_linear(q, w, [out], ws)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay()
+torch.cuda.synchronize()
+first = [o.clone() for _, _, o in jobs]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, o) and a.abs().sum() > 0 for a, (_, _, o) in zip(first, jobs))
+assert qkn.read_device_status(ws) == qkn.OK
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
+
+
+def test_calls_on_a_given_stream():
+    """``stream`` names the stream; the work waits for what is enqueued there and for nothing else."""
+    m, n, k = 40, 300, 512
+    a, w = operands(m, n, k, seed=6)
+    want = torch.empty((m, n), dtype=torch.float32, device="cuda")
+    ws = workspace()
+    qkn.fp8_linear(a, w, [want], ws)
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    x = hidden(m, k, torch.float32, 6)
+    late = torch.zeros_like(x)
+    q, out = qkn.Fp8Rows.empty(m, k), torch.empty_like(want)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)
+        late.copy_(x)
+    qkn.norm_quant(late, q, stream=st)
+    qkn.fp8_linear(q, w, [out], ws, stream=st)
+    st.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that element and byte offsets pass 2^31 and 2^32."""
+    m, k, n, ld = 70000, 128, 64, 65536
+    w = operands(1, n, k, seed=7)[1]
+    wide = torch.empty((m, ld), dtype=torch.float8_e4m3fn, device="cuda")        # 4.6e9 codes
+    x = hidden(m, k, torch.bfloat16, 7)
+    buf = torch.empty((m, ld // 2), dtype=torch.bfloat16, device="cuda")         # 2.3e9 elements
+    far, out = buf[:, 1000:1000 + k], buf[:, 2000:2000 + n]
+    far.copy_(x)
+    q = qkn.Fp8Rows(wide, torch.empty((1, m), dtype=torch.float32, device="cuda"), k)
+    qkn.norm_quant(far, q)
+    qkn.fp8_linear(q, w, [out], workspace())
+    torch.cuda.synchronize()
+    for rows in (slice(0, 300), slice(m - 300, m)):
+        codes, scale = host(wide[rows, :k]), host(q.scale[:, rows])
+        check_codes(codes, scale, host(x[rows]), 0)
+        av, wv = oracle.row_values(codes, scale), oracle.weight_values(host(w.codes[:, :k]), host(w.scale))
+        check_product(host(out[rows]), av @ wv.T, np.abs(av) @ np.abs(wv).T, k, torch.bfloat16)
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_tensors_on_another_device_than_the_current_one():
+    a, w = operands(40, 300, 512, seed=8)
+    want = torch.empty((40, 300), device="cuda")
+    qkn.fp8_linear(a, w, [want], workspace())
+    other = torch.device("cuda", 1)
+    a1 = qkn.Fp8Rows(a.codes.to(other), a.scale.to(other), a.cols)
+    w1 = qkn.Fp8Weight(w.codes.to(other), w.scale.to(other), w.cols)
+    out = torch.empty((40, 300), device=other)
+    qkn.fp8_linear(a1, w1, [out], torch.zeros(256, dtype=torch.uint8, device=other))
+    torch.cuda.synchronize(other)
+    assert torch.equal(out.cpu(), want.cpu())
+    with pytest.raises(ValueError):
+        qkn.fp8_linear(a1, w, [out], workspace())
