@@ -6,7 +6,8 @@
 // and code = e4m3(y / s).  All in fp32: the only roundings to fewer bits are the stored h, the optional
 // y and the codes.  The codes are formed as y * (1 / s): the reciprocal's rounding moves a value by at
 // most 2^-23 of itself, which changes a code only where y / s lies that close to the middle between
-// two codes.
+// two codes, either of which is then as near.  (A correctly rounded quotient, two more operations a
+// value, costs a tenth of the time where there is no norm: 54 us for 49 on the weight below.)
 #include <cuda_fp8.h>
 
 #include "common.cuh"
