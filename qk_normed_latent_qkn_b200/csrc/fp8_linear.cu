@@ -7,7 +7,7 @@
 //
 // Two kernels, both fed by TMA (128-byte swizzled boxes of 128 codes, which zero-fill whatever lies
 // behind the last row or column, so no size needs to be a multiple of anything):
-//   * linear_pair_kernel, many rows: pairs of CTAs share a tile of 256 rows x 256 columns
+//   * linear_pair_kernel, many rows: pairs of CTAs share a tile of 256 rows x 256 or 128 columns
 //     (cta_group::2), persistent over the tiles;
 //   * linear_split_kernel, few tiles: a tile is 128 columns of the product x 16 to 128 rows.  Up to 64
 //     rows the weight's columns take the tensor core's M and the rows its N; 128 rows take M themselves,
@@ -50,19 +50,19 @@ __device__ __forceinline__ float load_early(const float* p) {
   return v;
 }
 
-// One warp's 32 rows x 256 / sizeof(O) columns of the product pass through `box` (8 KB of shared memory)
-// from lanes that hold a row each to lanes that write 256 consecutive bytes of a row: straight from the
+// One warp's 32 rows x ROW / sizeof(O) columns of the product pass through `box` (ROW = 128 or 256 bytes a row)
+// from lanes that hold a row each to lanes that write ROW consecutive bytes of a row: straight from the
 // registers every lane's 16 bytes would be a half-written sector of another row.  The 16-byte pieces of
 // row r are permuted by r % 8, which keeps both sides free of bank conflicts.
-constexpr int kBoxRow = 256, kBoxBytes = 32 * kBoxRow;
+constexpr int kBoxBytes = 32 * 256;
 
-template <typename O>
+template <typename O, int ROW>
 __device__ __forceinline__ void fill_box(uint8_t* box, const float* v) {
   constexpr int E = 16 / (int)sizeof(O);
   const int lane = threadIdx.x & 31;
-  uint8_t* row = box + lane * kBoxRow;
+  uint8_t* row = box + lane * ROW;
 #pragma unroll
-  for (int u = 0; u < 16; ++u) {
+  for (int u = 0; u < ROW / 16; ++u) {
     uint4 w;
     if constexpr (sizeof(O) == 4) {
       w = make_uint4(__float_as_uint(v[u * E]), __float_as_uint(v[u * E + 1]), __float_as_uint(v[u * E + 2]),
@@ -79,26 +79,27 @@ __device__ __forceinline__ void fill_box(uint8_t* box, const float* v) {
   __syncwarp();
 }
 
-template <typename O>
+template <typename O, int ROW>
 __device__ __forceinline__ void write_box(const Fp8LinearArgs& p, const uint8_t* box, int row0, int col0) {
-  constexpr int E = 16 / (int)sizeof(O), COLS = 16 * E;
+  constexpr int E = 16 / (int)sizeof(O), PIECES = ROW / 16, COLS = PIECES * E;
   const int lane = threadIdx.x & 31;
   if (col0 < p.n) {
     int o = 0;
     while (col0 >= p.outs[o].end) ++o;
     const int rows = min(32, p.m - row0);
     if (col0 + COLS <= p.outs[o].end && wide_ok<O, E>(p.outs[o])) {
-      O* dst = static_cast<O*>(p.outs[o].out) + (col0 - p.outs[o].begin) + (lane & 15) * E;
-      for (int r = lane >> 4; r < rows; r += 2)
+      const int u = lane % PIECES;
+      O* dst = static_cast<O*>(p.outs[o].out) + (col0 - p.outs[o].begin) + u * E;
+      for (int r = lane / PIECES; r < rows; r += 32 / PIECES)
         *reinterpret_cast<uint4*>(dst + (row0 + r) * p.outs[o].ld) =
-            *reinterpret_cast<const uint4*>(box + r * kBoxRow + (((lane & 15) ^ (r & 7)) << 4));
+            *reinterpret_cast<const uint4*>(box + r * ROW + ((u ^ (r & 7)) << 4));
     } else {   // a destination ends inside the box, or its rows are not 16-byte aligned: element by element
       for (int e = lane; e < COLS && col0 + e < p.n; e += 32) {
         while (col0 + e >= p.outs[o].end) ++o;
         O* dst = static_cast<O*>(p.outs[o].out) + (col0 + e - p.outs[o].begin);
         for (int r = 0; r < rows; ++r)
           dst[(row0 + r) * p.outs[o].ld] =
-              *reinterpret_cast<const O*>(box + r * kBoxRow + (((e / E) ^ (r & 7)) << 4) + (e % E) * sizeof(O));
+              *reinterpret_cast<const O*>(box + r * ROW + (((e / E) ^ (r & 7)) << 4) + (e % E) * sizeof(O));
       }
     }
   }
@@ -106,29 +107,46 @@ __device__ __forceinline__ void write_box(const Fp8LinearArgs& p, const uint8_t*
 }
 
 // ---------------------------------------------------------------- many rows: CTA pairs
-constexpr int kPairM = 256, kPairN = 256;       // tile of a pair
-constexpr int kPairStages = 5;
-constexpr int kPairStageBytes = 2 * kTileBytes; // this CTA's 128 rows of A and 128 of W
-constexpr int kPairWarps = 8;                   // epilogue warps, each 32 rows x 128 columns
+// A pair's tile halves what each SM has to fetch of the weight (32 KB a block of K for 256 x 256 outputs,
+// and the L2 link of an SM brings about 64 bytes a cycle).  The scales of a block enter in fp32, so every
+// block's sums leave tensor memory: the MMAs of a block (512 cycles of an SM at 256 columns) fill one
+// accumulator while eight warps promote the other.  That promotion bounds the kernel: 835 cycles a block
+// on a B200, 683 without its FMAs, 607 without it.  8192 x 25152 x 4096: 765 to 900 us, 1.9 to 2.2 PFLOP/s
+// at 1.4 to 1.6 GHz, the power cap's doing; 4096 x 4096 x 16384: 270 to 315 us.  Sixteen promoting warps
+// were slower (they leave 96 registers each), as were half-width accumulators and packed FMAs.
+constexpr int kPairM = 256;                     // rows of a pair's tile
+constexpr int kPairWarps = 8;                   // epilogue warps, each 32 rows x half the tile's columns
 constexpr int kPairThreads = 64 + 32 * kPairWarps;
-constexpr int kPairCols = 128;                  // columns of an epilogue warp
 constexpr int kPairGroupM = 16;                 // row tiles that are walked before the next column tile
 constexpr int kLoadCols = 16;                   // columns of one TMEM load
 
+// N columns of a pair's tile: 256, or 128 where that fills the waves better.
+template <int N>
+struct PairCfg {
+  static constexpr int kHalfBytes = N / 2 * kRowBytes;            // this CTA's half of the tile's weight rows
+  static constexpr int kStageBytes = kTileBytes + kHalfBytes;     // and its 128 rows of A
+  static constexpr int kStages = N == 256 ? 5 : 6;
+  static constexpr int kAccs = 512 / N;                           // accumulators in tensor memory
+  static constexpr int kCols = N / 2;                             // columns of an epilogue warp
+  static constexpr int kBoxOff = kStages * kStageBytes;
+  static constexpr int kBarOff = kBoxOff + kPairWarps * kBoxBytes;
+  static constexpr int kSmem = 1024 + kBarOff + 256;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
 
+template <int S, int A>
 struct PairBars {
-  uint64_t full[kPairStages], empty[kPairStages];
-  uint64_t t_full[2], t_empty[2];
+  uint64_t full[S], empty[S];
+  uint64_t t_full[A], t_empty[A];
   uint64_t drained;                             // used once a wait has run out: the MMAs in flight are done
   uint32_t tmem;
 };
-constexpr int kPairBoxOff = kPairStages * kPairStageBytes;
-constexpr int kPairBarOff = kPairBoxOff + kPairWarps * kBoxBytes;
-constexpr int kPairSmem = 1024 + kPairBarOff + (int)sizeof(PairBars);
-static_assert(kPairSmem <= 227 * 1024, "shared memory of a CTA");
 
+template <int N>
 struct TileWalk {
   int mt, nt;
+  __device__ __forceinline__ explicit TileWalk(const Fp8LinearArgs& p)
+      : mt((p.m + kPairM - 1) / kPairM), nt((p.n + N - 1) / N) {}
   __device__ __forceinline__ void of(int t, int& m, int& n) const {
     const int g = t / (kPairGroupM * nt);
     const int rows = min(kPairGroupM, mt - g * kPairGroupM);
@@ -139,23 +157,25 @@ struct TileWalk {
 };
 
 // Warps: 0 producer, 1 MMA (the even CTA issues for both), 2-9 epilogue (each CTA its 128 rows; warps
-// 2-5 the tile's first 128 columns, 6-9 the others).
-template <typename O>
+// 2-5 the first half of the tile's columns, 6-9 the second).
+template <int N, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ Fp8LinearArgs p, const __grid_constant__ LinearMaps maps) {
+  using C = PairCfg<N>;
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
-  PairBars& bars = *reinterpret_cast<PairBars*>(smem + kPairBarOff);
+  auto& bars = *reinterpret_cast<PairBars<C::kStages, C::kAccs>*>(smem + C::kBarOff);
+  static_assert(sizeof(bars) <= 256, "barriers");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const uint32_t stages = smem_u32(smem);
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kPairStages; ++i) {
+    for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&bars.full[i]), 1);
       mbar_init(smem_u32(&bars.empty[i]), 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::kAccs; ++i) {
       mbar_init(smem_u32(&bars.t_full[i]), 1);
       mbar_init(smem_u32(&bars.t_empty[i]), 2 * kPairWarps);   // of both CTAs
     }
@@ -176,23 +196,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   pdl_trigger();
   pdl_wait();
 
-  const TileWalk walk{(p.m + kPairM - 1) / kPairM, (p.n + kPairN - 1) / kPairN};
+  const TileWalk<N> walk(p);
   const int tiles = walk.mt * walk.nt;   // (the launcher checks that they fit)
   const int blocks = (p.k + kFp8Group - 1) / kFp8Group;
   const int pairs = gridDim.x >> 1;
   bool ok = true;
 
   if (warp == 0) {
-    RingPos<kPairStages> ring;
+    RingPos<C::kStages> ring;
     for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
       int m, n;
       walk.of(t, m, n);
-      const int y_a = m * kPairM + (int)rank * 128, y_w = n * kPairN + (int)rank * 128;
+      const int y_a = m * kPairM + (int)rank * 128, y_w = n * N + (int)rank * (N / 2);
       for (int b = 0; b < blocks; ++b) {
         if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
         const uint32_t full = smem_u32(&bars.full[ring.slot]);
-        if (rank == 0) mbar_arrive_expect_tx_elect(full, 2 * kPairStageBytes);
-        const uint32_t dst = stages + ring.slot * kPairStageBytes;
+        if (rank == 0) mbar_arrive_expect_tx_elect(full, 2 * C::kStageBytes);
+        const uint32_t dst = stages + ring.slot * C::kStageBytes;
         const uint32_t bar = mapa_shared(full, 0);
         tma_load_2d_pair_elect(dst, &maps.a, b * kFp8Group, y_a, bar);
         tma_load_2d_pair_elect(dst + kTileBytes, &maps.w, b * kFp8Group, y_w, bar);
@@ -201,16 +221,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     // the last uses of the stages end before this CTA does: their commits arrive here (after a wait that ran
     // out, what this pair's copies still bring; the even CTA waits, the odd one for it)
-    for (int i = 0; i < kPairStages; ++i) {
+    for (int i = 0; i < C::kStages; ++i) {
       if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
       if (!ok && rank == 0) (void)mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase ^ 1u, kWaitCycles);
       ring.next();
     }
   } else if (warp == 1 && rank == 0) {
-    constexpr uint32_t idesc = idesc_e4m3(256, 256);
+    constexpr uint32_t idesc = idesc_e4m3(256, N);
     const uint64_t d_a = smem_desc(stages, 16, 1024), d_w = smem_desc(stages + kTileBytes, 16, 1024);
-    RingPos<kPairStages> ring;
-    RingPos<2> acc;
+    RingPos<C::kStages> ring;
+    RingPos<C::kAccs> acc;
     for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs)
       for (int b = 0; b < blocks; ++b) {
         if (!mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles) ||
@@ -219,10 +239,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint64_t at = (uint64_t)((ring.slot * kPairStageBytes) >> 4);
+        const uint64_t at = (uint64_t)((ring.slot * C::kStageBytes) >> 4);
 #pragma unroll
         for (int s = 0; s < kFp8Group / kKStep; ++s)
-          mma_e4m3_pair_elect(tmem + acc.slot * kPairN, d_a + at + s * kDescStep, d_w + at + s * kDescStep, idesc,
+          mma_e4m3_pair_elect(tmem + acc.slot * N, d_a + at + s * kDescStep, d_w + at + s * kDescStep, idesc,
                               s > 0);
         mma_commit_group2_elect(smem_u32(&bars.empty[ring.slot]), 3);
         mma_commit_group2_elect(smem_u32(&bars.t_full[acc.slot]), 3);
@@ -235,29 +255,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else if (warp >= 2) {
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* box = smem + kPairBoxOff + (warp - 2) * kBoxBytes;
-    const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + half * kPairCols;
-    RingPos<2> acc;
-    float total[kPairCols];
+    uint8_t* box = smem + C::kBoxOff + (warp - 2) * kBoxBytes;
+    const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + half * C::kCols;
+    RingPos<C::kAccs> acc;
+    float total[C::kCols];
     // One block of K: its sums leave TMEM 16 columns at a time, the next ones on their way while these
     // enter the total.  (Single FMAs: as packed pairs they need the same FMA cycles and, with the moves
     // that pair up registers, more instructions.)
     auto enter = [&](float s) {
       if (ok && !mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) ok = false;
       tc_fence_after();
-      const uint32_t at = tq + acc.slot * kPairN;
-      constexpr int N = kPairCols / kLoadCols;
+      const uint32_t at = tq + acc.slot * N;
+      constexpr int L = C::kCols / kLoadCols;
       uint32_t v[2][kLoadCols];
       tmem_ld16(at, v[0]);
       tmem_wait_ld(v[0]);
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        if (c < N - 1) tmem_ld16(at + (c + 1) * kLoadCols, v[(c + 1) & 1]);
+      for (int c = 0; c < L; ++c) {
+        if (c < L - 1) tmem_ld16(at + (c + 1) * kLoadCols, v[(c + 1) & 1]);
 #pragma unroll
         for (int e = 0; e < kLoadCols; ++e)
           total[c * kLoadCols + e] = fmaf(__uint_as_float(v[c & 1][e]), s, total[c * kLoadCols + e]);
-        if (c < N - 1) tmem_wait_ld(v[(c + 1) & 1]);
-        if (c == N - 2) {   // everything is out of TMEM
+        if (c < L - 1) tmem_wait_ld(v[(c + 1) & 1]);
+        if (c == L - 2) {   // everything is out of TMEM
           tc_fence_before();
           __syncwarp();
           // (relaxed: what the arrival stands for, the loads from TMEM, is complete, and a release would
@@ -273,11 +293,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       int m, n;
       walk.of(t, m, n);
       const float* sa = p.a_scale + min(m * kPairM + (int)rank * 128 + quad * 32 + lane, p.m - 1);
-      const float* sw = p.w_scale + (int64_t)min(2 * n + half, (p.n - 1) / kFp8Group) * blocks;
+      const float* sw = p.w_scale + (int64_t)min((n * N + half * C::kCols) / kFp8Group, (p.n - 1) / kFp8Group) * blocks;
       const int b1 = blocks > 1 ? 1 : 0;
       float s0 = __ldg(sa) * __ldg(sw), s1 = __ldg(sa + b1 * p.ld_as) * __ldg(sw + b1);
 #pragma unroll
-      for (int i = 0; i < kPairCols; ++i) total[i] = 0.f;
+      for (int i = 0; i < C::kCols; ++i) total[i] = 0.f;
       for (int b = 0; b < blocks; b += 2) {
         const int b2 = min(b + 2, blocks - 1), b3 = min(b + 3, blocks - 1);
         const float a2 = load_early(sa + b2 * p.ld_as), w2 = load_early(sw + b2);
@@ -289,11 +309,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
       if (ok) {
         walk.of(t, m, n);
-        constexpr int COLS = kBoxRow / (int)sizeof(O);
+        constexpr int ROW = C::kCols * (int)sizeof(O) < 256 ? C::kCols * (int)sizeof(O) : 256;
+        constexpr int COLS = ROW / (int)sizeof(O);
 #pragma unroll
-        for (int c = 0; c < kPairCols; c += COLS) {
-          fill_box<O>(box, total + c);
-          write_box<O>(p, box, m * kPairM + (int)rank * 128 + quad * 32, n * kPairN + half * kPairCols + c);
+        for (int c = 0; c < C::kCols; c += COLS) {
+          fill_box<O, ROW>(box, total + c);
+          write_box<O, ROW>(p, box, m * kPairM + (int)rank * 128 + quad * 32, n * N + half * C::kCols + c);
         }
       }
     }
@@ -344,6 +365,10 @@ struct SplitBars {
   uint32_t tmem;
 };
 
+// Bound by memory or, in short calls, by the chain of one load, MMA, promotion and join: 32 x 25152 x 4096
+// takes 22 us on a B200 (103 MB of weight; 7 TB/s once it streams, 5 us to start and end), 64 x 4096 x 16384
+// 19, 1 x 576 x 2048 3.7.  Splitting K over a cluster needs no workspace and no atomics, and the parts are
+// added in rank order: the same bits every time.
 // One tile: 128 columns of the product for NT rows.  Cluster rank r takes the r-th part of K's blocks.
 // Warps: 0 producer, 1 MMA, 2 on: epilogue.
 template <int NT, typename O>
@@ -574,20 +599,21 @@ bool codes_map(CUtensorMap* m, const uint8_t* codes, int k, int rows, int64_t ld
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <typename O>
+template <int N, typename O>
 cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   LinearMaps maps;
-  if (!codes_map(&maps.a, a.a, a.k, a.m, a.lda, 128) || !codes_map(&maps.w, a.w, a.k, a.n, a.ldw, 128))
+  if (!codes_map(&maps.a, a.a, a.k, a.m, a.lda, 128) || !codes_map(&maps.w, a.w, a.k, a.n, a.ldw, N / 2))
     return cudaErrorInvalidValue;
   static PerDeviceOnce attrs;
   cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(linear_pair_kernel<O>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+    return cudaFuncSetAttribute(linear_pair_kernel<N, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                PairCfg<N>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)ceil_div(a.m, kPairM) * ceil_div(a.n, kPairN);
+  const int64_t tiles = (int64_t)ceil_div(a.m, kPairM) * ceil_div(a.n, N);
   if (tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_chained(linear_pair_kernel<O>, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, st, a, maps);
+  return launch_chained(linear_pair_kernel<N, O>, dim3(2 * pairs), dim3(kPairThreads), PairCfg<N>::kSmem, st, a, maps);
 }
 
 // Clusters of `size` CTAs that the device holds at once, one CTA per SM: fewer than its SMs' worth, because a
@@ -675,24 +701,30 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int dev, int sms, cudaStream_t 
   return cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, O>, a, maps, split, row_tiles);
 }
 
-// Whether more than 64 rows are better served by pairs of CTAs.  Both kernels walk their tiles in waves
-// over the SMs; the constants (nanoseconds for a block of K, and for a tile's start and end) are from
-// B200 runs: the estimates are within 15% of the times below, and the choice falls right for all.
-//   rows x columns x K         pairs    split
-//   128 x 25152 x 4096         38 us    37 us
-//   256 x 25152 x 4096         39       55
-//   256 x  4096 x 16384        62       30
-//   1024 x 4096 x 16384        68      100
-//   333 x  1000 x 1960         14        7.5
-//   2048 x  576 x 4096         20       17
+// Which kernel takes more than 64 rows.  All three walk their tiles in waves over the SMs; the constants
+// (nanoseconds for a start, for a tile's start and end, and for a block of K) are from B200 runs: the
+// estimates are within a fifth of the times below, and the choice falls on the shortest but for near ties.
+//   rows x columns x K       pairs of 256   pairs of 128   split
+//   128 x 25152 x 4096            38 us          38 us      37 us
+//   256 x 25152 x 4096            39             38         55
+//   512 x  4096 x 16384           62             46         52
+//   256 x  4096 x 16384           60             45         30
+//   1024 x 4096 x 16384           66            103        100
+//   2048 x  576 x 4096            20             15         18
+//   333 x  1000 x 1960            16             10         7.5
+//   4096 x 4096 x 16384          303            374          -
+enum class Kernel { kPair256, kPair128, kSplit };
+
 template <typename O>
-bool pairs_pay(int64_t m, int64_t n, int blocks, int dev, int sms) {
-  const int64_t pair_tiles = (int64_t)ceil_div(m, kPairM) * ceil_div(n, kPairN);
-  const int64_t pair_waves = ceil_div(pair_tiles, sms / 2);
+Kernel choose(int64_t m, int64_t n, int blocks, int dev, int sms) {
+  const int64_t row_tiles = ceil_div(m, kPairM);
+  const int64_t wide = 4000 + ceil_div(row_tiles * ceil_div(n, 256), sms / 2) * (1500 + (int64_t)blocks * 480);
+  const int64_t narrow = 4000 + ceil_div(row_tiles * ceil_div(n, 128), sms / 2) * (1500 + (int64_t)blocks * 335);
   const int64_t tiles = (int64_t)ceil_div(m, 128) * ceil_div(n, 128);
-  const int split = split_of<128, O>(tiles, blocks, dev, sms);
-  const int64_t waves = ceil_div(tiles * split, sms);
-  return 4000 + pair_waves * (1500 + (int64_t)blocks * 480) < waves * (5000 + (int64_t)ceil_div(blocks, split) * 380);
+  const int parts = split_of<128, O>(tiles, blocks, dev, sms);
+  const int64_t split = ceil_div(tiles * parts, sms) * (5000 + (int64_t)ceil_div(blocks, parts) * 380);
+  if (split <= wide && split <= narrow) return Kernel::kSplit;
+  return narrow < wide ? Kernel::kPair128 : Kernel::kPair256;
 }
 
 template <typename O>
@@ -703,8 +735,11 @@ cudaError_t launch(const Fp8LinearArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   if (a.m > 64) {
     if ((e = split_attrs<128, O>()) != cudaSuccess) return e;   // (the estimate asks for the kernel's occupancy)
-    return pairs_pay<O>(a.m, a.n, ceil_div(a.k, kFp8Group), dev, sms) ? launch_pair<O>(a, sms, st)
-                                                                      : launch_split<128, O>(a, dev, sms, st);
+    switch (choose<O>(a.m, a.n, ceil_div(a.k, kFp8Group), dev, sms)) {
+      case Kernel::kPair256: return launch_pair<256, O>(a, sms, st);
+      case Kernel::kPair128: return launch_pair<128, O>(a, sms, st);
+      case Kernel::kSplit: return launch_split<128, O>(a, dev, sms, st);
+    }
   }
   // the smallest of 16, 32 and 64 rows that holds them all: every tile reads its weight rows once
   if (a.m > 32) return launch_split<64, O>(a, dev, sms, st);

@@ -208,6 +208,8 @@ LINEAR = [  # m, n, k, widths
     (513, 1536, 512, [1024, 8, 504]), (1000, 3333, 260, [1111, 1111, 1111]), (2049, 520, 256, [520]),
     (4, 4096, 16384, [4096]), (48, 12288, 512, [8192, 4096]), (1, 25152, 640, [16384, 8192, 512, 64]),
     (700, 2560, 128, [320] * 8),
+    # several tiles for every pair of CTAs, of 256 columns (three waves) and of 128 (two)
+    (2049, 5000, 300, [4000, 1000]), (700, 6200, 300, [6200]),
 ]
 
 
