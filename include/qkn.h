@@ -492,7 +492,7 @@ typedef struct {
  *   h = x, or x + residual rounded to dtype and written to residual_out;
  *   y = h * gamma / sqrt(mean(h^2) + eps), or y = h without gamma (no norm);
  *   per row and block of 128 columns: scale = max(max|y| / 448, 2^-100), code = y / scale rounded to
- *   the nearest e4m3 (ties to even).
+ *   the nearest e4m3 (the quotient taken as y times the scale's reciprocal).
  * fp32 arithmetic; the sum of squares must stay in fp32's range.  A NaN makes its block of codes (with
  * gamma: its row) NaN, an infinity without gamma its block; other rows are not touched by it.
  *   x         [n, ld_x] dtype, ld_x >= d;  residual, residual_out [n, d] dtype, both or neither
@@ -505,8 +505,8 @@ QKN_EXPORT qkn_status qkn_norm_quant(qkn_dtype dtype, const void* x, int64_t ld_
                       void* stream);
 
 /* qkn_quant_weight — quantise a weight [q->rows, q->cols] (row-major, dense) of type dtype: per block of 128 x 128
- * scale = max(max|w| / 448, 2^-100), code = w / scale rounded to the nearest e4m3.  A NaN or an infinity makes its
- * block NaN. */
+ * scale = max(max|w| / 448, 2^-100), code = w / scale rounded to the nearest e4m3, as in qkn_norm_quant.  A NaN or
+ * an infinity makes its block NaN. */
 QKN_EXPORT qkn_status qkn_quant_weight(qkn_dtype dtype, const void* w, const qkn_fp8_weight* q, void* stream);
 
 /* qkn_fp8_linear — out = A W^T for rows and a weight in 8 bits:

@@ -346,6 +346,7 @@ def gqa_decode(dims: Dims, cache: GqaCache, q, q_rope, gamma_q, gamma_qr, block_
 FP8_GROUP = 128            # columns (and, in a weight, rows) that share a scale
 _E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+_cuda_device, _cuda_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 class Fp8Rows:
@@ -376,8 +377,8 @@ class Fp8Rows:
         return q
 
     def c(self) -> _Fp8Rows:
-        return _Fp8Rows(self.codes.data_ptr(), self.scale.data_ptr(), self.rows, self.cols, self.codes.shape[1],
-                        self.scale.shape[1])
+        codes, scale = self.codes, self.scale
+        return _Fp8Rows(codes.data_ptr(), scale.data_ptr(), self.rows, self.cols, codes.shape[1], scale.shape[1])
 
 
 class Fp8Weight:
@@ -415,19 +416,16 @@ def _type_code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _call_on(device: torch.device, stream, fn, *args) -> int:
-    """``fn(*args, stream handle)`` with ``device`` current: the library launches on the current device."""
-    index = device.index
-    if index is None or device.type != "cuda":
+def _call_on(index: int, stream, fn, *args) -> int:
+    """``fn(*args, stream handle)`` with device ``index`` current: the library launches on the current device."""
+    if index < 0 or index == _cuda_device():   # (CPU tensors: only calls that launch nothing come through)
         return fn(*args, _stream(stream))
-    if index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return fn(*args, _stream(stream))
-    return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
+    with torch.cuda.device(index):
+        return fn(*args, _stream(stream))
 
 
-def _beside(t: torch.Tensor, x: torch.Tensor, shape, dev, what: str) -> int:
-    if t.shape != shape or t.dtype != x.dtype or not t.is_contiguous() or t.device != dev:
+def _beside(t: torch.Tensor, x: torch.Tensor, shape, index: int, what: str) -> int:
+    if t.shape != shape or t.dtype != x.dtype or not t.is_contiguous() or t.get_device() != index:
         raise ValueError(f"{what} is dense, of x's shape, type and device")
     return t.data_ptr()
 
@@ -436,64 +434,77 @@ def norm_quant(x, q: Fp8Rows, gamma=None, eps: float = 1e-6, residual=None, resi
                stream=None) -> None:
     """Residual addition, RMSNorm (with ``gamma``) and quantisation of rows to 8 bits (see qkn_norm_quant): ``x``
     [n, d], its rows contiguous; ``residual`` / ``residual_out`` / ``y`` dense [n, d] of x's type or None."""
-    dtype, dev, shape = _type_code(x, "x"), x.device, x.shape
+    dtype, index, shape = _type_code(x, "x"), x.get_device(), x.shape
     if len(shape) != 2:
         raise ValueError("x is [n, d] with contiguous rows")
     n, d = shape
     ld_x, step = x.stride()
     if step != 1 and d != 1:
         raise ValueError("x is [n, d] with contiguous rows")
-    codes = q.codes
-    if q.rows != n or q.cols != d or codes.device != dev:
+    codes, scale = q.codes, q.scale
+    if q.rows != n or q.cols != d or codes.get_device() != index:
         raise ValueError("q holds n rows of d values on x's device")
     g = r = h = v = None
     if gamma is not None:
-        if gamma.dtype != _FP32 or gamma.shape != (d,) or not gamma.is_contiguous() or gamma.device != dev:
+        if gamma.dtype != _FP32 or gamma.shape != shape[1:] or not gamma.is_contiguous() or gamma.get_device() != index:
             raise ValueError("gamma is a float32 [d] on x's device")
         g = gamma.data_ptr()
     if residual is not None:
-        r = _beside(residual, x, shape, dev, "residual")
+        r = _beside(residual, x, shape, index, "residual")
     if residual_out is not None:
-        h = r if residual_out is residual else _beside(residual_out, x, shape, dev, "residual_out")
+        h = r if residual_out is residual else _beside(residual_out, x, shape, index, "residual_out")
     if y is not None:
-        v = _beside(y, x, shape, dev, "y")
-    scale = q.scale
+        v = _beside(y, x, shape, index, "y")
     rows = _Fp8Rows(codes.data_ptr(), scale.data_ptr(), n, d, codes.shape[1], scale.shape[1])
-    status = _call_on(dev, stream, _lib.qkn_norm_quant, dtype, x.data_ptr(), ld_x if n > 1 else d, r, g, eps, h, v,
-                      ctypes.byref(rows))
+    if n == 1:
+        ld_x = d
+    if stream is None and index >= 0 and index == _cuda_device():
+        status = _lib.qkn_norm_quant(dtype, x.data_ptr(), ld_x, r, g, eps, h, v, ctypes.byref(rows),
+                                     _cuda_stream(index))
+    else:
+        status = _call_on(index, stream, _lib.qkn_norm_quant, dtype, x.data_ptr(), ld_x, r, g, eps, h, v,
+                          ctypes.byref(rows))
     if status != OK:
         raise QknError(status, "qkn_norm_quant")
 
 
 def quant_weight(w, q: Fp8Weight, stream=None) -> None:
     """Quantise a dense weight [n, k] to 8 bits with a scale for each block of 128 x 128 (see qkn_quant_weight)."""
-    dtype, dev = _type_code(w, "w"), w.device
-    if w.shape != (q.rows, q.cols) or not w.is_contiguous() or q.codes.device != dev:
+    dtype, index = _type_code(w, "w"), w.get_device()
+    if w.shape != (q.rows, q.cols) or not w.is_contiguous() or q.codes.get_device() != index:
         raise ValueError("w is a dense [n, k], q holds as much on its device")
-    _check(_call_on(dev, stream, _lib.qkn_quant_weight, dtype, w.data_ptr(), ctypes.byref(q.c())),
-           "qkn_quant_weight")
+    status = _call_on(index, stream, _lib.qkn_quant_weight, dtype, w.data_ptr(), ctypes.byref(q.c()))
+    if status != OK:
+        raise QknError(status, "qkn_quant_weight")
 
 
 def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=None) -> None:
     """out = A W^T from 8 bits (see qkn_fp8_linear); ``outs``: up to MAX_OUTS tensors [a.rows, width] of one type,
     their rows contiguous, that take the product's columns in order."""
-    n_outs, dev, rows = len(outs), a.codes.device, a.rows
+    n_outs, index, rows = len(outs), a.codes.get_device(), a.rows
     if not 1 <= n_outs <= MAX_OUTS:
         raise ValueError(f"outs holds 1 to {MAX_OUTS} tensors")
+    kind = outs[0].dtype
     dtype = _type_code(outs[0], "outs")
     arr = (_OutCols * n_outs)()
     for t, o in zip(outs, arr):
-        if t.dim() != 2 or t.shape[0] != rows or t.dtype != outs[0].dtype or t.device != dev:
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != rows or t.dtype != kind or t.get_device() != index:
             raise ValueError("an output is [rows, width], all of one type, on the codes' device")
         ld, step = t.stride()
-        width = t.shape[1]
+        width = shape[1]
         if step != 1 and width != 1:
             raise ValueError("an output's rows are contiguous")
         o.out, o.cols, o.ld = t.data_ptr(), width, ld if rows > 1 else width
-    if w.codes.device != dev or workspace.device != dev:
+    if w.codes.get_device() != index or workspace.get_device() != index:
         raise ValueError("all tensors are on one device")
-    _check(_call_on(dev, stream, _lib.qkn_fp8_linear, ctypes.byref(a.c()), ctypes.byref(w.c()), dtype, n_outs, arr,
-                    workspace.data_ptr(), workspace.nbytes), "qkn_fp8_linear")
+    ca, cw, ws, ws_bytes = ctypes.byref(a.c()), ctypes.byref(w.c()), workspace.data_ptr(), workspace.nbytes
+    if stream is None and index >= 0 and index == _cuda_device():
+        status = _lib.qkn_fp8_linear(ca, cw, dtype, n_outs, arr, ws, ws_bytes, _cuda_stream(index))
+    else:
+        status = _call_on(index, stream, _lib.qkn_fp8_linear, ca, cw, dtype, n_outs, arr, ws, ws_bytes)
+    if status != OK:
+        raise QknError(status, "qkn_fp8_linear")
 
 
 def read_device_status(workspace: torch.Tensor, stream=None) -> int:
