@@ -418,10 +418,12 @@ def _type_code(t: torch.Tensor, what: str) -> int:
 
 def _call_on(index: int, stream, fn, *args) -> int:
     """``fn(*args, stream handle)`` with device ``index`` current: the library launches on the current device."""
-    if index < 0 or index == _cuda_device():   # (CPU tensors: only calls that launch nothing come through)
+    if index < 0:                              # CPU tensors: only calls that launch nothing come through
         return fn(*args, _stream(stream))
+    if index == _cuda_device():
+        return fn(*args, _cuda_stream(index) if stream is None else _stream(stream))
     with torch.cuda.device(index):
-        return fn(*args, _stream(stream))
+        return fn(*args, _cuda_stream(index) if stream is None else _stream(stream))
 
 
 def _beside(t: torch.Tensor, x: torch.Tensor, shape, index: int, what: str) -> int:
