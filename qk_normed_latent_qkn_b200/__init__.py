@@ -346,6 +346,7 @@ def gqa_decode(dims: Dims, cache: GqaCache, q, q_rope, gamma_q, gamma_qr, block_
 FP8_GROUP = 128            # columns (and, in a weight, rows) that share a scale
 _E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32}
+_OUT_ARRAYS = tuple(_OutCols * i for i in range(MAX_OUTS + 1))
 _cuda_device, _cuda_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
@@ -358,7 +359,8 @@ class Fp8Rows:
     def __init__(self, codes: torch.Tensor, scale: torch.Tensor, cols: int):
         if codes.dtype != _E4M3 or codes.dim() != 2 or not codes.is_contiguous():
             raise ValueError("codes is a contiguous float8_e4m3fn [rows, ld]")
-        if scale.dtype != _FP32 or scale.dim() != 2 or not scale.is_contiguous() or scale.device != codes.device:
+        if (scale.dtype != _FP32 or scale.dim() != 2 or not scale.is_contiguous()
+                or scale.get_device() != codes.get_device()):
             raise ValueError("scale is a contiguous float32 [ceil(cols / 128), ld_scale] on the codes' device")
         rows, ld = codes.shape
         blocks, ld_scale = scale.shape
@@ -391,8 +393,9 @@ class Fp8Weight:
         if codes.dtype != _E4M3 or codes.dim() != 2 or not codes.is_contiguous():
             raise ValueError("codes is a contiguous float8_e4m3fn [rows, ld]")
         rows, ld = codes.shape
-        if (not 1 <= cols <= ld or scale.dtype != _FP32 or not scale.is_contiguous() or scale.device != codes.device
-                or tuple(scale.shape) != ((rows + 127) // FP8_GROUP, (cols + 127) // FP8_GROUP)):
+        if (not 1 <= cols <= ld or scale.dtype != _FP32 or not scale.is_contiguous()
+                or scale.get_device() != codes.get_device()
+                or scale.shape != ((rows + 127) // FP8_GROUP, (cols + 127) // FP8_GROUP)):
             raise ValueError("scale is a contiguous float32 [ceil(rows / 128), ceil(cols / 128)] on the codes' device")
         self.codes, self.scale, self.rows, self.cols = codes, scale, rows, cols
 
@@ -488,7 +491,7 @@ def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=N
         raise ValueError(f"outs holds 1 to {MAX_OUTS} tensors")
     kind = outs[0].dtype
     dtype = _type_code(outs[0], "outs")
-    arr = (_OutCols * n_outs)()
+    arr = _OUT_ARRAYS[n_outs]()
     for t, o in zip(outs, arr):
         shape = t.shape
         if len(shape) != 2 or shape[0] != rows or t.dtype != kind or t.get_device() != index:
