@@ -498,8 +498,9 @@ typedef struct {
  *   x         [n, ld_x] dtype, ld_x >= d;  residual, residual_out [n, d] dtype, both or neither
  *   gamma     [d] fp32 or NULL;  y [n, d] dtype or NULL: the normalised rows, rounded to dtype
  *   residual_out may be residual, or x where ld_x = d; y may be x where ld_x = d and residual is NULL
- * rows == 0 is a no-op.  Any d up to 2^30; rows of at most 16384 values (32768 where every row is
- * 16-byte aligned and d a multiple of 8) are read once.  Returns QKN_ERR_INVALID_ARG for a bad size, pointer or alignment. */
+ * rows == 0 is a no-op.  Any d up to 2^30; rows of at most 32768 values (16384 in fp32
+ * where they are not 16-byte aligned) are read once.  Returns
+ * QKN_ERR_INVALID_ARG for a bad size, pointer or alignment. */
 QKN_EXPORT qkn_status qkn_norm_quant(qkn_dtype dtype, const void* x, int64_t ld_x, const void* residual,
                       const float* gamma, float eps, void* residual_out, void* y, const qkn_fp8_rows* q,
                       void* stream);

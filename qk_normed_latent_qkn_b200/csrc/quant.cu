@@ -51,11 +51,10 @@ __device__ __forceinline__ float block_sum(float v) {
 // One CTA per row (without a norm: per 4096 columns of a row), and the row read once: every thread keeps
 // its values of h until the sum of squares is known, as they are stored, so that in bf16 32 registers
 // suffice and an SM holds all its 2048 threads.  Bound by memory: 16384 x 4096 bf16 with the residual
-// (472 MB) takes 72 us on a B200, 6.57 TB/s; 82 to 90 us with h kept in fp32.  Two layouts:
-//   * pieces of 8 (rows that are 16-byte aligned, d a multiple of 8): thread t holds the pieces t, t + T,
-//     ..., of T threads, so 16 neighbouring lanes hold a block of 128 and its maximum takes 4 exchanges;
-//   * elements (anything else): a warp holds the blocks w, w + W, ..., lane l the elements l + 32 e, so
-//     that every access is a run of 32 elements wherever it starts.
+// (472 MB) takes 72 us on a B200, 6.57 TB/s; 82 to 90 us with h kept in fp32.  Thread t holds the pieces of
+// 8 values t, t + T, ..., of T threads, so 16 neighbouring lanes hold a block of 128 and its maximum takes 4
+// exchanges.  bf16 rows that are not 16-byte aligned are read in aligned chunks and shifted into place;
+// fp32 ones go by elements, a warp per block of 128.
 constexpr int kPiece = 8;
 constexpr int kMaxThreads = 1024;
 
@@ -70,6 +69,83 @@ struct Piece {
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
     for (int e = 0; e < (int)sizeof(T) / 2; ++e) reinterpret_cast<uint4*>(p)[e] = u[e];
+  }
+  // The first `valid` values from p, which need not be aligned: the 16-byte chunks that hold them, shifted
+  // into place, where all of these lie within [lo, hi), the array's bounds; else element by element.
+  __device__ __forceinline__ void load_any(const T* p, int valid, const T* lo, const T* hi) {
+    constexpr int NW = sizeof(T) * 2, NC = NW / 4 + 1;   // words of a piece, chunks that hold it
+    const uintptr_t off = reinterpret_cast<uintptr_t>(p) & 15;
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+    uint32_t w[4 * NC];
+    if (valid == kPiece && reinterpret_cast<const char*>(q) >= reinterpret_cast<const char*>(lo) &&
+        reinterpret_cast<const char*>(q + NC) <= reinterpret_cast<const char*>(hi)) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const uint4 c = q[i];
+        w[4 * i] = c.x, w[4 * i + 1] = c.y, w[4 * i + 2] = c.z, w[4 * i + 3] = c.w;
+      }
+      if (off & 8) {
+#pragma unroll
+        for (int i = 0; i < NW + 2; ++i) w[i] = w[i + 2];
+      }
+      if (off & 4) {
+#pragma unroll
+        for (int i = 0; i < NW + 1; ++i) w[i] = w[i + 1];
+      }
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < NW; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (uint32_t)(off & 2) * 8);
+      }
+    } else {
+      float f[kPiece];
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) f[e] = e < valid ? to_f32(p[e]) : 0.f;
+      set(f);   // (exact: the values are T's)
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < NW / 4; ++i) u[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
+  // The first `valid` values to p, in the widest stores that its alignment allows.
+  __device__ __forceinline__ void store_any(T* p, int valid) const {
+    uint32_t w[sizeof(T) * 2];
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[4 * i] = u[i].x, w[4 * i + 1] = u[i].y, w[4 * i + 2] = u[i].z, w[4 * i + 3] = u[i].w;
+    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    if (valid < kPiece) {
+      float f[kPiece];
+      values(f);
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e)
+        if (e < valid) p[e] = from_f32<T>(f[e]);
+    } else if (off == 0) {
+      store(p);
+    } else if constexpr (sizeof(T) == 4) {
+      if (off == 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint4*>(p + 2) = make_uint4(w[2], w[3], w[4], w[5]);
+        *reinterpret_cast<uint2*>(p + 6) = make_uint2(w[6], w[7]);
+      } else {
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+#pragma unroll
+        for (int i = 1; i < 7; i += 2) *reinterpret_cast<uint2*>(p + i) = make_uint2(w[i], w[i + 1]);
+        *reinterpret_cast<uint32_t*>(p + 7) = w[7];
+      }
+    } else {
+      if (off & 2) {
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)w[0];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t*>(p + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+        *reinterpret_cast<uint16_t*>(p + 7) = (uint16_t)(w[3] >> 16);
+      } else if (off & 4) {
+        *reinterpret_cast<uint32_t*>(p) = w[0];
+        *reinterpret_cast<uint2*>(p + 2) = make_uint2(w[1], w[2]);
+        *reinterpret_cast<uint32_t*>(p + 6) = w[3];
+      } else {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
+      }
+    }
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -114,6 +190,19 @@ __device__ __forceinline__ uint2 codes_of(const float (&v)[kPiece], float rs) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
+// A piece's codes (rows of codes are 16-byte aligned); ANY: only the first `valid` of them.
+template <bool ANY>
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int valid) {
+  if (!ANY || valid >= kPiece) {
+    *reinterpret_cast<uint2*>(p) = c;
+  } else {
+    const uint64_t b = (uint64_t)c.y << 32 | c.x;
+#pragma unroll
+    for (int e = 0; e < kPiece - 1; ++e)
+      if (e < valid) p[e] = (uint8_t)(b >> (8 * e));
+  }
+}
+
 __device__ __forceinline__ float piece_max(const float (&v)[kPiece]) {
   float m = fabsf(v[0]);
 #pragma unroll
@@ -127,7 +216,8 @@ __device__ __forceinline__ float half_warp_max(float m) {
   return m;
 }
 
-template <typename T, int PIECES, int THREADS, int CTAS>
+// ANY: rows of any alignment and width; else 16-byte aligned rows of whole pieces.
+template <typename T, int PIECES, int THREADS, int CTAS, bool ANY>
 __global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQuantArgs a, int parts) {
   pdl_trigger();
   pdl_wait();
@@ -143,15 +233,30 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQu
   Piece<T> h[PIECES];   // as stored: h is rounded to T, so nothing is lost
 #pragma unroll
   for (int c = 0; c < PIECES; ++c) {
-    if (j0 + c * step < d) h[c].load(x + j0 + c * step);
-    else h[c].zero();
+    const int j = j0 + c * step;
+    if (j >= d) {
+      h[c].zero();
+    } else if constexpr (ANY) {
+      const T* x0 = static_cast<const T*>(a.x);
+      h[c].load_any(x + j, min(d - j, kPiece), x0, x0 + (a.n - 1) * a.ld_x + d);
+    } else {
+      h[c].load(x + j);
+    }
   }
   if (a.residual) {
     const T* r = static_cast<const T*>(a.residual) + i * d;
     Piece<T> t[PIECES];
 #pragma unroll
-    for (int c = 0; c < PIECES; ++c)
-      if (j0 + c * step < d) t[c].load(r + j0 + c * step);
+    for (int c = 0; c < PIECES; ++c) {
+      const int j = j0 + c * step;
+      if (j >= d) continue;
+      if constexpr (ANY) {
+        const T* r0 = static_cast<const T*>(a.residual);
+        t[c].load_any(r + j, min(d - j, kPiece), r0, r0 + (int64_t)a.n * d);
+      } else {
+        t[c].load(r + j);
+      }
+    }
 #pragma unroll
     for (int c = 0; c < PIECES; ++c)
       if (j0 + c * step < d) {
@@ -161,7 +266,9 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQu
 #pragma unroll
         for (int e = 0; e < kPiece; ++e) f[e] += g[e];
         h[c].set(f);
-        h[c].store(static_cast<T*>(a.residual_out) + i * d + j0 + c * step);
+        T* out = static_cast<T*>(a.residual_out) + i * d + j0 + c * step;
+        if constexpr (ANY) h[c].store_any(out, min(d - j0 - c * step, kPiece));
+        else h[c].store(out);
       }
   }
   float inv = 1.f;
@@ -183,7 +290,8 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQu
     h[c].values(f);
     if (a.gamma && j < d) {
       Piece<float> g;
-      g.load(a.gamma + j);
+      if constexpr (ANY) g.load_any(a.gamma + j, min(d - j, kPiece), a.gamma, a.gamma + d);
+      else g.load(a.gamma + j);
       float gf[kPiece];
       g.values(gf);
 #pragma unroll
@@ -191,50 +299,52 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQu
     }
     const float s = scale_of(half_warp_max(piece_max(f)));
     if (j < d) {
-      *reinterpret_cast<uint2*>(a.codes + i * a.ld + j) = codes_of(f, 1.f / s);
+      store_codes<ANY>(a.codes + i * a.ld + j, codes_of(f, 1.f / s), d - j);
       if (j % kFp8Group == 0) a.scale[j / kFp8Group * a.ld_scale + i] = s;
       if (a.y) {
         Piece<T> y;
         y.set(f);
-        y.store(static_cast<T*>(a.y) + i * d + j);
+        if constexpr (ANY) y.store_any(static_cast<T*>(a.y) + i * d + j, min(d - j, kPiece));
+        else y.store(static_cast<T*>(a.y) + i * d + j);
       }
     }
   }
 }
 
-template <typename T, int BLOCKS, int THREADS>
+// fp32 rows of any alignment: element loads are whole 128-byte lines, pieces of 8 are not (2048 x 4095: 25 us
+// on a B200, 34 in shifted pieces; in bf16 24.4 and 23.9, and 177 and 138 at 16384 rows).
+template <int BLOCKS, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_quant_elements_kernel(NormQuantArgs a) {
   pdl_trigger();
   pdl_wait();
   const int64_t i = blockIdx.x;
   const int d = a.d, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const T* x = static_cast<const T*>(a.x) + i * a.ld_x;
+  const float* x = static_cast<const float*>(a.x) + i * a.ld_x;
   float h[BLOCKS][4];
 #pragma unroll
   for (int c = 0; c < BLOCKS; ++c)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int j = (warp + c * warps) * kFp8Group + e * 32 + lane;
-      h[c][e] = j < d ? to_f32(x[j]) : 0.f;
+      h[c][e] = j < d ? x[j] : 0.f;
     }
   if (a.residual) {
-    const T* r = static_cast<const T*>(a.residual) + i * d;
+    const float* r = static_cast<const float*>(a.residual) + i * d;
     float t[BLOCKS][4];
 #pragma unroll
     for (int c = 0; c < BLOCKS; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = (warp + c * warps) * kFp8Group + e * 32 + lane;
-        t[c][e] = j < d ? to_f32(r[j]) : 0.f;
+        t[c][e] = j < d ? r[j] : 0.f;
       }
 #pragma unroll
     for (int c = 0; c < BLOCKS; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int j = (warp + c * warps) * kFp8Group + e * 32 + lane;
-        const T u = from_f32<T>(h[c][e] + t[c][e]);
-        h[c][e] = to_f32(u);
-        if (j < d) static_cast<T*>(a.residual_out)[i * d + j] = u;
+        h[c][e] += t[c][e];
+        if (j < d) static_cast<float*>(a.residual_out)[i * d + j] = h[c][e];
       }
   }
   if (a.gamma) {
@@ -265,7 +375,7 @@ __global__ void __launch_bounds__(THREADS) norm_quant_elements_kernel(NormQuantA
       const int j = g * kFp8Group + e * 32 + lane;
       if (j < d) {
         a.codes[i * a.ld + j] = code_of(h[c][e] * rs);
-        if (a.y) static_cast<T*>(a.y)[i * d + j] = from_f32<T>(h[c][e]);
+        if (a.y) static_cast<float*>(a.y)[i * d + j] = h[c][e];
       }
     }
     if (lane == 0) a.scale[g * a.ld_scale + i] = s;
@@ -329,40 +439,40 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_long_kernel(NormQuantA
 }
 
 // ---------------------------------------------------------------- weights
-// One CTA per block of 128 x 128, read once.  WIDE: in pieces of 8 (16-byte aligned rows), 16 lanes along a
-// row; else a warp along a row, lane l with the elements l + 32 e.  Every thread keeps what it read, as it
-// was read, until the block's maximum is known.  Bound by memory: several CTAs share an SM so that one
+// One CTA per block of 128 x 128, read once in pieces of 8, 16 lanes along a row (ANY: rows of any alignment
+// and width; else 16-byte aligned rows of whole pieces).  Every thread keeps what it read, as it was read, until the block's maximum is known.  Bound by memory: several CTAs share an SM so that one
 // block's loads run beside another's stores, and what a thread keeps decides how many.  bf16, 25152 x 4096
 // (309 MB) on a B200: 49 us, 6.3 TB/s, with three CTAs; 58 with two, 59 with four, which spill.
-constexpr int kWeightThreads = 512, kWeightElementThreads = 1024;
+constexpr int kWeightThreads = 512;
 
 // Largest magnitude of the CTA's threads.
-template <int THREADS>
 __device__ __forceinline__ float block_max(float m) {
-  __shared__ float part[THREADS / 32];
+  __shared__ float part[kWeightThreads / 32];
   m = warp_max_nan(m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
   __syncthreads();
-  m = part[threadIdx.x & (THREADS / 32 - 1)];
+  m = part[threadIdx.x & (kWeightThreads / 32 - 1)];
 #pragma unroll
-  for (int o = THREADS / 64; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int o = kWeightThreads / 64; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   return m;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 2 ? 3 : 2) quant_weight_pieces_kernel(QuantWeightArgs a, int k_blocks) {
+template <typename T, bool ANY>
+__global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 2 ? 3 : 2)
+    quant_weight_kernel(QuantWeightArgs a, int k_blocks) {
   pdl_trigger();
   pdl_wait();
   constexpr int STEP = kWeightThreads / 16, ROWS = kFp8Group / STEP;
   const int col = (int)(blockIdx.x % k_blocks) * kFp8Group + (int)(threadIdx.x & 15) * kPiece;
   const int64_t row = (int64_t)(blockIdx.x / k_blocks) * kFp8Group + (threadIdx.x >> 4);
-  const T* w = static_cast<const T*>(a.w) + row * a.k + col;
+  const T* w0 = static_cast<const T*>(a.w);
+  const T* w = w0 + row * a.k + col;
   Piece<T> v[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
-    const bool in = row + r * STEP < a.n && col < a.k;
-    if (in) v[r].load(w + (int64_t)r * STEP * a.k);
-    else v[r].zero();
+    if (row + r * STEP >= a.n || col >= a.k) v[r].zero();
+    else if constexpr (ANY) v[r].load_any(w + (int64_t)r * STEP * a.k, min(a.k - col, kPiece), w0, w0 + (int64_t)a.n * a.k);
+    else v[r].load(w + (int64_t)r * STEP * a.k);
   }
   float m = 0.f;
 #pragma unroll
@@ -371,42 +481,14 @@ __global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 2 ? 3 : 2) quant_
     v[r].values(f);
     m = max_nan(m, piece_max(f));
   }
-  const float s = scale_of(block_max<kWeightThreads>(m)), rs = 1.f / s;
+  const float s = scale_of(block_max(m)), rs = 1.f / s;
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     if (row + r * STEP >= a.n || col >= a.k) continue;
     float f[kPiece];
     v[r].values(f);
-    *reinterpret_cast<uint2*>(a.codes + (row + r * STEP) * a.ld + col) = codes_of(f, rs);
+    store_codes<ANY>(a.codes + (row + r * STEP) * a.ld + col, codes_of(f, rs), a.k - col);
   }
-  if (threadIdx.x == 0) a.scale[blockIdx.x] = s;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kWeightElementThreads) quant_weight_elements_kernel(QuantWeightArgs a, int k_blocks) {
-  pdl_trigger();
-  pdl_wait();
-  constexpr int STEP = kWeightElementThreads / 32, ROWS = kFp8Group / STEP;
-  const int col = (int)(blockIdx.x % k_blocks) * kFp8Group + (int)(threadIdx.x & 31);
-  const int64_t row = (int64_t)(blockIdx.x / k_blocks) * kFp8Group + (threadIdx.x >> 5);
-  const T* w = static_cast<const T*>(a.w) + row * a.k + col;
-  float v[ROWS][4], m = 0.f;
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[r][e] = row + r * STEP < a.n && col + e * 32 < a.k ? to_f32(w[(int64_t)r * STEP * a.k + e * 32]) : 0.f;
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m = max_nan(m, fabsf(v[r][e]));
-  const float s = scale_of(block_max<kWeightElementThreads>(m)), rs = 1.f / s;
-#pragma unroll
-  for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (row + r * STEP < a.n && col + e * 32 < a.k)
-        a.codes[(row + r * STEP) * a.ld + col + e * 32] = code_of(v[r][e] * rs);
   if (threadIdx.x == 0) a.scale[blockIdx.x] = s;
 }
 
@@ -419,39 +501,49 @@ int round32(int64_t v) { return (int)((v + 31) / 32 * 32); }
 template <typename T>
 constexpr int kCtasOf = sizeof(T) == 2 ? 8 : 4;
 
-template <typename T>
-cudaError_t launch_norm(const NormQuantArgs& a, cudaStream_t st) {
-  constexpr int kCtas = kCtasOf<T>;
+template <typename T, bool ANY>
+cudaError_t launch_norm_pieces(const NormQuantArgs& a, cudaStream_t st) {
+  constexpr int kCtas = ANY ? kCtasOf<T> / 2 : kCtasOf<T>;
   const dim3 grid(a.n);
-  const bool wide = a.d % kPiece == 0 && a.ld_x * sizeof(T) % 16 == 0 && on16(a.x) && on16(a.residual) &&
-                    on16(a.residual_out) && on16(a.gamma) && on16(a.y);
-  const int pieces = (a.d + kPiece - 1) / kPiece, blocks = (a.d + kFp8Group - 1) / kFp8Group;
-  if (wide && !a.gamma) {   // every block of 128 stands alone: rows in parts of up to 4096 columns
+  const int pieces = (a.d + kPiece - 1) / kPiece;
+  if (!a.gamma) {   // every block of 128 stands alone: rows in parts of up to 4096 columns
     const int per = (pieces + 1) / 2, threads = per < 256 ? round32(per) : 256;
     const int parts = (pieces + 2 * threads - 1) / (2 * threads);
     if ((int64_t)a.n * parts <= INT32_MAX)
-      return launch_chained(norm_quant_pieces_kernel<T, 2, 256, kCtas>, dim3(a.n * parts), dim3(threads), 0, st, a,
+      return launch_chained(norm_quant_pieces_kernel<T, 2, 256, kCtas, ANY>, dim3(a.n * parts), dim3(threads), 0, st, a,
                             parts);
   }
-  if (wide && pieces <= 4 * kMaxThreads) {
-    // few rows: one piece per thread, the shortest chain; many: CTAs of 256 threads with 2 pieces, a full SM's
-    // threads of them
-    const bool few = a.n <= 512;
-    if (pieces <= (few ? kMaxThreads : 256))
-      return launch_chained(norm_quant_pieces_kernel<T, 1, kMaxThreads, 1>, grid, dim3(round32(pieces)), 0, st, a, 1);
-    if (!few && pieces <= 2 * 256)
-      return launch_chained(norm_quant_pieces_kernel<T, 2, 256, kCtas>, grid, dim3(round32((pieces + 1) / 2)), 0, st, a, 1);
-    if (pieces <= 2 * kMaxThreads)
-      return launch_chained(norm_quant_pieces_kernel<T, 2, kMaxThreads, kCtas / 4>, grid, dim3(round32((pieces + 1) / 2)), 0, st,
-                            a, 1);
-    return launch_chained(norm_quant_pieces_kernel<T, 4, kMaxThreads, 1>, grid, dim3(round32((pieces + 3) / 4)), 0, st,
+  // few rows: one piece per thread, the shortest chain; many: CTAs of 256 threads with 2 pieces, an SM full of them
+  const bool few = a.n <= 512;
+  if (pieces <= (few ? kMaxThreads : 256))
+    return launch_chained(norm_quant_pieces_kernel<T, 1, kMaxThreads, 1, ANY>, grid, dim3(round32(pieces)), 0, st, a, 1);
+  if (!few && pieces <= 2 * 256)
+    return launch_chained(norm_quant_pieces_kernel<T, 2, 256, kCtas, ANY>, grid, dim3(round32((pieces + 1) / 2)), 0, st,
                           a, 1);
+  if (pieces <= 2 * kMaxThreads)
+    return launch_chained(norm_quant_pieces_kernel<T, 2, kMaxThreads, (kCtas >= 4 ? kCtas / 4 : 1), ANY>, grid,
+                          dim3(round32((pieces + 1) / 2)), 0, st, a, 1);
+  return launch_chained(norm_quant_pieces_kernel<T, 4, kMaxThreads, 1, ANY>, grid, dim3(round32((pieces + 3) / 4)), 0,
+                        st, a, 1);
+}
+
+template <typename T>
+cudaError_t launch_norm(const NormQuantArgs& a, cudaStream_t st) {
+  const bool aligned = a.d % kPiece == 0 && a.ld_x * sizeof(T) % 16 == 0 && on16(a.x) && on16(a.residual) &&
+                       on16(a.residual_out) && on16(a.gamma) && on16(a.y);
+  if (a.d > 4 * kMaxThreads * kPiece)
+    return launch_chained(norm_quant_long_kernel<T>, dim3(a.n), dim3(kMaxThreads), 0, st, a);
+  if (aligned) return launch_norm_pieces<T, false>(a, st);
+  if constexpr (sizeof(T) == 4) {
+    const int blocks = (a.d + kFp8Group - 1) / kFp8Group;
+    if (blocks <= 2 * 32)
+      return launch_chained(norm_quant_elements_kernel<2, kMaxThreads>, dim3(a.n), dim3((blocks + 1) / 2 * 32), 0, st, a);
+    if (blocks <= 8 * 16)
+      return launch_chained(norm_quant_elements_kernel<8, 512>, dim3(a.n), dim3((blocks + 7) / 8 * 32), 0, st, a);
+    return launch_chained(norm_quant_long_kernel<T>, dim3(a.n), dim3(kMaxThreads), 0, st, a);
+  } else {
+    return launch_norm_pieces<T, true>(a, st);
   }
-  if (blocks <= 2 * 32)
-    return launch_chained(norm_quant_elements_kernel<T, 2, kMaxThreads>, grid, dim3((blocks + 1) / 2 * 32), 0, st, a);
-  if (blocks <= 8 * 16)
-    return launch_chained(norm_quant_elements_kernel<T, 8, 512>, grid, dim3((blocks + 7) / 8 * 32), 0, st, a);
-  return launch_chained(norm_quant_long_kernel<T>, grid, dim3(kMaxThreads), 0, st, a);
 }
 
 template <typename T>
@@ -459,10 +551,9 @@ cudaError_t launch_weight(const QuantWeightArgs& a, cudaStream_t st) {
   const int k_blocks = (int)(((int64_t)a.k + kFp8Group - 1) / kFp8Group);
   const int64_t ctas = (int64_t)k_blocks * (((int64_t)a.n + kFp8Group - 1) / kFp8Group);
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)ctas);
-  if (a.k % kPiece == 0 && on16(a.w))
-    return launch_chained(quant_weight_pieces_kernel<T>, grid, dim3(kWeightThreads), 0, st, a, k_blocks);
-  return launch_chained(quant_weight_elements_kernel<T>, grid, dim3(kWeightElementThreads), 0, st, a, k_blocks);
+  const dim3 grid((unsigned)ctas), block(kWeightThreads);
+  return a.k % kPiece == 0 && on16(a.w) ? launch_chained(quant_weight_kernel<T, false>, grid, block, 0, st, a, k_blocks)
+                                        : launch_chained(quant_weight_kernel<T, true>, grid, block, 0, st, a, k_blocks);
 }
 
 }  // namespace

@@ -113,6 +113,34 @@ def test_norm_quant_in_place_and_strided_rows(dtype, d):
         check_codes(host(q3.codes[:, :d]), host(q3.scale[:, :n]), y64, d)
 
 
+def shifted(t, by):
+    """A dense copy of t that starts ``by`` elements behind an aligned address."""
+    flat = torch.empty(t.numel() + by, dtype=t.dtype, device="cuda")
+    flat[by:] = t.reshape(-1)
+    return flat[by:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("by", [1, 2, 3, 4, 7])
+@pytest.mark.parametrize("n,d", [(3, 264), (600, 1000), (2, 20000)])
+def test_unaligned_bases(n, d, by, dtype):
+    """Every array of a call starts off the 16-byte grid, by amounts of their own."""
+    x, res = hidden(n, d, dtype, by), hidden(n, d, dtype, by + 1)
+    gamma = shifted((1 + 0.1 * torch.randn(d, generator=torch.Generator().manual_seed(by))).cuda(), by)
+    q = qkn.Fp8Rows.empty(n, d)
+    h, y = shifted(torch.zeros_like(x), by), shifted(torch.zeros_like(x), by + 2)
+    qkn.norm_quant(shifted(x, by + 1), q, gamma=gamma, residual=shifted(res, by + 3), residual_out=h, y=y)
+    total = host(x) + host(res)
+    assert np.all(np.abs(host(h) - total) <= np.abs(total) * (HALF_STEP[dtype] + U) + 1e-40)
+    y64 = oracle.rms_norm(host(h), host(gamma), 1e-6)
+    check_codes(host(q.codes[:, :d]), host(q.scale[:, :n]), y64, d)
+    assert np.all(np.abs(host(y) - y64) <= np.abs(y64) * (HALF_STEP[dtype] + (d // 256 + 40) * U))
+    w, w1 = qkn.Fp8Weight.empty(n, d), qkn.Fp8Weight.empty(n, d)
+    qkn.quant_weight(x, w)
+    qkn.quant_weight(shifted(x, by), w1)
+    assert torch.equal(w.scale, w1.scale) and torch.equal(w.codes.view(torch.uint8)[:, :d], w1.codes.view(torch.uint8)[:, :d])
+
+
 @pytest.mark.parametrize("d", [256, 250])
 def test_norm_quant_of_zeros_infinities_and_nan(d):
     """A zero row has zero codes and the least scale; a NaN or an infinity spoils its block (with gamma, its row)
