@@ -93,7 +93,38 @@ __device__ __forceinline__ void write_box(const Fp8LinearArgs& p, const uint8_t*
       for (int r = lane / PIECES; r < rows; r += 32 / PIECES)
         *reinterpret_cast<uint4*>(dst + (row0 + r) * p.outs[o].ld) =
             *reinterpret_cast<const uint4*>(box + r * ROW + ((u ^ (r & 7)) << 4));
-    } else {   // a destination ends inside the box, or its rows are not 16-byte aligned: element by element
+    } else if (col0 + COLS <= p.outs[o].end) {
+      // Rows off the 16-byte grid: lane u writes the u-th aligned 16 bytes of a row, shifted out of two pieces,
+      // and the E elements at the row's two ends go one to a lane.
+      const int u = lane % PIECES;
+      for (int r = lane / PIECES; r < rows; r += 32 / PIECES) {
+        O* dst = static_cast<O*>(p.outs[o].out) + (row0 + r) * p.outs[o].ld + (col0 - p.outs[o].begin);
+        const uint8_t* from = box + r * ROW;
+        const uint32_t s = (0u - (uint32_t)reinterpret_cast<uintptr_t>(dst)) & 15;   // bytes before the grid
+        if (u < PIECES - 1 || s == 0) {
+          const uint4 a = *reinterpret_cast<const uint4*>(from + ((u ^ (r & 7)) << 4));
+          const uint4 b = *reinterpret_cast<const uint4*>(from + ((min(u + 1, PIECES - 1) ^ (r & 7)) << 4));
+          uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+          if (s & 8) {
+#pragma unroll
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+          }
+          if (s & 4) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+          }
+          if constexpr (sizeof(O) == 2) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (s & 2) * 8);
+          }
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(dst) + s + 16 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (s != 0 && u < E) {
+          const int e = u < (int)(s / sizeof(O)) ? u : COLS - E + u;
+          dst[e] = *reinterpret_cast<const O*>(from + (((e / E) ^ (r & 7)) << 4) + (e % E) * sizeof(O));
+        }
+      }
+    } else {   // a destination ends inside the box: element by element
       for (int e = lane; e < COLS && col0 + e < p.n; e += 32) {
         while (col0 + e >= p.outs[o].end) ++o;
         O* dst = static_cast<O*>(p.outs[o].out) + (col0 + e - p.outs[o].begin);
