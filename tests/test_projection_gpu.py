@@ -330,6 +330,40 @@ def test_norm_and_product_captured_replayed_and_on_two_streams(m, n, k):
     assert qkn.read_device_status(ws) == qkn.OK
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 576, 2048), (40, 9472, 512), (100, 2000, 1024), (333, 1000, 1960),
+                                   (600, 9472, 1024), (4096, 1024, 512)])
+def test_one_buffer_rewritten_between_back_to_back_products(m, n, k):
+    """Norm and product in a chain with nothing else on the stream, the rows in 8 bits (and the weight) in one
+    buffer that every pair rewrites: each kernel starts while the one before it runs, and must see its values."""
+    rounds = 12
+    xs = [hidden(m, k, torch.bfloat16, s) * 2.0 ** (s % 5) for s in range(rounds)]
+    ws_ = [(torch.randn((n, k), generator=torch.Generator().manual_seed(s)) * 2.0 ** (s % 3)).cuda() for s in range(3)]
+    gamma = torch.ones(k, device="cuda")
+    ws = workspace()
+
+    def chain(sync):
+        q, w = qkn.Fp8Rows.empty(m, k), qkn.Fp8Weight.empty(n, k)
+        outs = [torch.empty((m, n), dtype=torch.float32, device="cuda") for _ in range(rounds)]
+        torch.cuda.synchronize()
+        for i in range(rounds):
+            if i % 4 == 0:
+                qkn.quant_weight(ws_[i // 4], w)
+            qkn.norm_quant(xs[i], q, gamma=gamma if i % 2 else None)
+            if sync:
+                torch.cuda.synchronize()
+            qkn.fp8_linear(q, w, [outs[i]], ws)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    want = chain(True)
+    for _ in range(4):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+    assert qkn.read_device_status(ws) == qkn.OK
+
+
 def test_first_calls_of_a_process_may_be_captured():
     """What the library sets up once per kernel and device happens inside a capture too."""
     code = """
