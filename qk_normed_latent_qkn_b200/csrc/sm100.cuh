@@ -517,11 +517,6 @@ __device__ __forceinline__ void tma_load_2d_pair_elect(uint32_t dst, const void*
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(cluster_bar)
       : "memory");
 }
-// Arrival that orders nothing: for "this thread has read what it wanted", when the values read are already in
-// registers.
-__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // Instruction descriptor for kind::f8f6f4 with e4m3 A/B (both K-major), fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
   return (1u << 4)                     // D format: f32 (A and B formats 0: e4m3)
