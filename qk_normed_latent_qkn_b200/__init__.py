@@ -419,10 +419,10 @@ def _type_code(t: torch.Tensor, what: str) -> int:
     return code
 
 
-def _call_on(index: int, stream, fn, *args) -> int:
+def _call_on(index: int, stream, rows: int, fn, *args) -> int:
     """``fn(*args, stream handle)`` with device ``index`` current: the library launches on the current device."""
-    if index < 0:                              # CPU tensors: only calls that launch nothing come through
-        return fn(*args, _stream(stream))
+    if index < 0:                              # CPU tensors: nothing that a kernel may read
+        return ERR_INVALID_ARG if rows else fn(*args, _stream(stream))
     if index == _cuda_device():
         return fn(*args, _cuda_stream(index) if stream is None else _stream(stream))
     with torch.cuda.device(index):
@@ -467,7 +467,7 @@ def norm_quant(x, q: Fp8Rows, gamma=None, eps: float = 1e-6, residual=None, resi
         status = _lib.qkn_norm_quant(dtype, x.data_ptr(), ld_x, r, g, eps, h, v, ctypes.byref(rows),
                                      _cuda_stream(index))
     else:
-        status = _call_on(index, stream, _lib.qkn_norm_quant, dtype, x.data_ptr(), ld_x, r, g, eps, h, v,
+        status = _call_on(index, stream, n, _lib.qkn_norm_quant, dtype, x.data_ptr(), ld_x, r, g, eps, h, v,
                           ctypes.byref(rows))
     if status != OK:
         raise QknError(status, "qkn_norm_quant")
@@ -478,7 +478,7 @@ def quant_weight(w, q: Fp8Weight, stream=None) -> None:
     dtype, index = _type_code(w, "w"), w.get_device()
     if w.shape != (q.rows, q.cols) or not w.is_contiguous() or q.codes.get_device() != index:
         raise ValueError("w is a dense [n, k], q holds as much on its device")
-    status = _call_on(index, stream, _lib.qkn_quant_weight, dtype, w.data_ptr(), ctypes.byref(q.c()))
+    status = _call_on(index, stream, q.rows, _lib.qkn_quant_weight, dtype, w.data_ptr(), ctypes.byref(q.c()))
     if status != OK:
         raise QknError(status, "qkn_quant_weight")
 
@@ -507,7 +507,7 @@ def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=N
     if stream is None and index >= 0 and index == _cuda_device():
         status = _lib.qkn_fp8_linear(ca, cw, dtype, n_outs, arr, ws, ws_bytes, _cuda_stream(index))
     else:
-        status = _call_on(index, stream, _lib.qkn_fp8_linear, ca, cw, dtype, n_outs, arr, ws, ws_bytes)
+        status = _call_on(index, stream, rows, _lib.qkn_fp8_linear, ca, cw, dtype, n_outs, arr, ws, ws_bytes)
     if status != OK:
         raise QknError(status, "qkn_fp8_linear")
 

@@ -171,6 +171,18 @@ def test_binding_refuses_tensors_that_do_not_fit():
         qkn.norm_quant(x, q, residual=x.clone())
 
 
+def test_binding_refuses_cpu_tensors():
+    """A kernel must not be handed host memory: refused before anything is launched."""
+    x = torch.zeros((4, 256))
+    q, w = qkn.Fp8Rows.empty(4, 256, "cpu"), qkn.Fp8Weight.empty(64, 256, "cpu")
+    for call in (lambda: qkn.norm_quant(x, q),
+                 lambda: qkn.quant_weight(torch.zeros((64, 256)), w),
+                 lambda: qkn.fp8_linear(q, w, [torch.zeros((4, 64))], torch.zeros(512, dtype=torch.uint8))):
+        with pytest.raises(qkn.QknError) as e:
+            call()
+        assert e.value.status == qkn.ERR_INVALID_ARG
+
+
 def test_holders_allocate_what_the_calls_need():
     q = qkn.Fp8Rows.empty(5, 300, "cpu")
     assert q.codes.shape == (5, 304) and q.scale.shape == (3, 8)
