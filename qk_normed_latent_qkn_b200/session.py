@@ -70,17 +70,21 @@ class DecodeSession:
         norm in front of them, ``w_in`` [H d_h + H d_R + r + d_R, D] with the rows of q, q^R, c and k^R in this order,
         ``w_out`` [D, H d_v] the output projection of the up-projected values (needs load_value_weights)."""
         d, dev = self.dims, self.device
-        self.gamma_x = to_device(gamma_x, torch.float32, dev)
-        self.w_in = self._quantised(w_in)
-        if self.w_in.rows != sum(self.projection_widths()) or self.w_in.cols != self.gamma_x.shape[0]:
+        gamma_x = to_device(gamma_x, torch.float32, dev)
+        if tuple(w_in.shape) != (sum(self.projection_widths()), gamma_x.shape[0]):
             raise ValueError("w_in is [H d_h + H d_R + r + d_R, D], gamma_x [D]")
-        self.w_out = None
-        if w_out is not None:
-            self.w_out = self._quantised(w_out)
-            if self.w_uv is None or self.w_out.cols != d.num_heads * self.w_uv.shape[-1]:
-                raise ValueError("w_out is [D, H d_v] for the value weights loaded before")
+        if w_out is not None and (self.w_uv is None or w_out.shape[1] != d.num_heads * self.w_uv.shape[-1]):
+            raise ValueError("w_out is [D, H d_v] for the value weights loaded before")
+        self.gamma_x, self.w_in = gamma_x, self._quantised(w_in)
+        self.w_out = None if w_out is None else self._quantised(w_out)
+        self.q = self.x8 = self.o8 = None              # sized by the weights
         self.proj_workspace = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
         workspace_init(self.proj_workspace)
+
+    def check_out_width(self) -> None:
+        """load_value_weights may have replaced the weights that load_projections was given w_out for."""
+        if self.w_out.cols != self.dims.num_heads * self.w_uv.shape[-1]:
+            raise ValueError("w_out was loaded for value weights of another width")
 
     def _quantised(self, w) -> Fp8Weight:
         w = to_device(w, self.dims.torch_dtype, self.device)
@@ -123,6 +127,9 @@ class DecodeSession:
         """The output projection: o_v [..., H, d_v] -> hidden states [n, D]."""
         if self.w_out is None:
             raise RuntimeError("project_out needs load_projections with w_out first")
+        self.check_out_width()
+        if o_v.shape[-1] != self.w_out.cols and o_v.shape[-2:] != (self.dims.num_heads, self.w_uv.shape[-1]):
+            raise ValueError("o_v is [..., H, d_v] or [..., H d_v]")
         rows = o_v.reshape(-1, self.w_out.cols)
         n = int(rows.shape[0])
         if self.o8 is None or self.o8.rows != n:

@@ -126,6 +126,7 @@ class LayerStep(DecodeStep):
                  ak_mode: int = AK_CACHE, head_tile: int = 0):
         if session.w_in is None or session.w_out is None:
             raise RuntimeError("LayerStep needs a session with load_projections (w_out included)")
+        session.check_out_width()
         d = session.dims
         dt, dev, i32 = d.torch_dtype, session.device, torch.int32
         n, width = batch * s_q, session.w_in.cols

@@ -133,3 +133,25 @@ def test_layer_calls_need_their_weights():
         LayerStep(s, 1, 1, 4)
     s.project(torch.ones((2, 64)))
     assert (s.q == 0).all() and s.device_status() == qkn.OK
+
+
+def test_projections_loaded_again_with_another_width():
+    """The buffers follow the weights, not the number of rows alone; and an output projection whose value weights were
+    replaced by others of another width is refused."""
+    s = session_from_inputs(make_inputs(WORKLOADS["tiny_f32"]))
+    rows, g = sum(s.projection_widths()), torch.Generator().manual_seed(5)
+    heads, d_v = s.dims.num_heads, s.w_uv.shape[-1]
+    for width in (64, 200, 136):
+        s.load_projections(torch.ones(width), torch.randn((rows, width), generator=g),
+                           torch.randn((width, heads * d_v), generator=g))
+        s.project(torch.randn((2, width), generator=g))
+        check_linear(s.x8, s.w_in, (s.q, s.q_rope, s.c_new, s.k_rope_new), torch.float32)
+        o_v = torch.randn((2, heads, d_v), generator=g).cuda()
+        hidden = s.project_out(o_v)
+        assert hidden.shape == (2, width)
+        check_linear(s.o8, s.w_out, [hidden], torch.float32)
+    s.load_value_weights(torch.randn((heads, s.dims.r_kv, 2 * d_v), generator=g))
+    with pytest.raises(ValueError):
+        s.project_out(torch.randn((1, heads, 2 * d_v), generator=g).cuda())
+    with pytest.raises(ValueError):
+        LayerStep(s, 1, 1, 4)
