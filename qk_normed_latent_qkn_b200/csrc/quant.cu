@@ -4,10 +4,8 @@
 // Mathematics.  h = x + r (rounded to the storage type, which is what the next layer reads back);
 // y = h * gamma * (mean(h^2) + eps)^-1/2; for every block of 128 columns s = max(max|y| / 448, 2^-100)
 // and code = e4m3(y / s).  All in fp32: the only roundings to fewer bits are the stored h, the optional
-// y and the codes.  The codes are formed as y * (1 / s): the reciprocal's rounding moves a value by at
-// most 2^-23 of itself, which changes a code only where y / s lies that close to the middle between
-// two codes, either of which is then as near.  (A correctly rounded quotient, two more operations a
-// value, costs a tenth of the time where there is no norm: 54 us for 49 on the weight below.)
+// y and the codes.  A code is the nearest e4m3 to the fp32 quotient y / s, taken without a division per
+// value: see Quotient.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -25,8 +23,39 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 __device__ __forceinline__ float scale_of(float amax) { return max_nan(amax / kFp8Top, kFp8Least); }
 
-__device__ __forceinline__ uint8_t code_of(float v) {
-  return (uint8_t)__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+// v / s for the values of a block from r = 1 / s: q = v r, corrected by its remainder, v - q s, times r
+// (Markstein's division).  It gives the code that the correctly rounded quotient gives, for every v and s: before
+// its last rounding it is within 2^-22 units of the last place of v / s, so the codes could part only where v / s
+// lies that close to a border between the fp32 numbers that round to the middle of two codes and their
+// neighbours; a test goes through all significands for which it does.  (Below a scale of 2^-93 a remainder may
+// underflow; a code can then differ where v / s is within 2^-16 units of such a border.)  v r alone gives
+// another code for 0.05 % of normal bf16 weights; it would take 71.4 us for 72.3 on the norm below, 48.2 for 52 on
+// the weight, and 12.2 for 13.1 on 1021 x 16384 bf16 without a norm (73.2, 53.7 and 13.4 without packed operations).
+struct Quotient {
+  float s, r;
+  // (an infinite scale has r = 0: finite values become 0, infinities NaN, and a remainder would spoil the former)
+  __device__ __forceinline__ explicit Quotient(float scale) : s(isinf(scale) ? 0.f : scale), r(1.f / scale) {}
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = v * r;
+    return fmaf(fmaf(-q, s, v), r, q);
+  }
+  // Two at once, in packed instructions.
+  __device__ __forceinline__ float2 operator()(float a, float b) const {
+    float2 o;
+    asm("{\n\t.reg .b64 v, s, r, q;\n\t"
+        "mov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\tmov.b64 r, {%5, %5};\n\t"
+        "mul.rn.f32x2 q, v, r;\n\t"
+        "fma.rn.f32x2 v, q, s, v;\n\t"
+        "fma.rn.f32x2 q, v, r, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "=f"(o.x), "=f"(o.y)
+        : "f"(a), "f"(b), "f"(-s), "f"(r));
+    return o;
+  }
+};
+
+__device__ __forceinline__ uint8_t code_of(float q) {
+  return (uint8_t)__nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
 __device__ __forceinline__ float warp_max_nan(float v) {
@@ -51,7 +80,7 @@ __device__ __forceinline__ float block_sum(float v) {
 // One CTA per row (without a norm: per 4096 columns of a row), and the row read once: every thread keeps
 // its values of h until the sum of squares is known, as they are stored, so that in bf16 32 registers
 // suffice and an SM holds all its 2048 threads.  Bound by memory: 16384 x 4096 bf16 with the residual
-// (472 MB) takes 72 us on a B200, 6.57 TB/s; 82 to 90 us with h kept in fp32.  Thread t holds the pieces of
+// (472 MB) takes 72.3 us on a B200, 6.53 TB/s; 82 to 90 us with h kept in fp32.  Thread t holds the pieces of
 // 8 values t, t + T, ..., of T threads, so 16 neighbouring lanes hold a block of 128 and its maximum takes 4
 // exchanges.  bf16 rows that are not 16-byte aligned are read in aligned chunks and shifted into place;
 // fp32 ones go by elements, a warp per block of 128.
@@ -182,11 +211,11 @@ struct Piece {
   }
 };
 
-__device__ __forceinline__ uint2 codes_of(const float (&v)[kPiece], float rs) {
+__device__ __forceinline__ uint2 codes_of(const float (&v)[kPiece], const Quotient& by) {
   uint32_t h[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    h[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * rs, v[2 * e + 1] * rs), __NV_SATFINITE, __NV_E4M3);
+    h[e] = __nv_cvt_float2_to_fp8x2(by(v[2 * e], v[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) norm_quant_pieces_kernel(NormQu
     }
     const float s = scale_of(half_warp_max(piece_max(f)));
     if (j < d) {
-      store_codes<ANY>(a.codes + i * a.ld + j, codes_of(f, 1.f / s), d - j);
+      store_codes<ANY>(a.codes + i * a.ld + j, codes_of(f, Quotient(s)), d - j);
       if (j % kFp8Group == 0) a.scale[j / kFp8Group * a.ld_scale + i] = s;
       if (a.y) {
         Piece<T> y;
@@ -369,12 +398,13 @@ __global__ void __launch_bounds__(THREADS) norm_quant_elements_kernel(NormQuantA
     float m = fabsf(h[c][0]);
 #pragma unroll
     for (int e = 1; e < 4; ++e) m = max_nan(m, fabsf(h[c][e]));
-    const float s = scale_of(warp_max_nan(m)), rs = 1.f / s;
+    const float s = scale_of(warp_max_nan(m));
+    const Quotient by(s);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int j = g * kFp8Group + e * 32 + lane;
       if (j < d) {
-        a.codes[i * a.ld + j] = code_of(h[c][e] * rs);
+        a.codes[i * a.ld + j] = code_of(by(h[c][e]));
         if (a.y) static_cast<float*>(a.y)[i * d + j] = h[c][e];
       }
     }
@@ -425,12 +455,13 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_long_kernel(NormQuantA
       }
       m = max_nan(m, fabsf(v[e]));
     }
-    const float s = scale_of(warp_max_nan(m)), rs = 1.f / s;
+    const float s = scale_of(warp_max_nan(m));
+    const Quotient by(s);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int64_t j = g * kFp8Group + e * 32 + lane;
       if (j < d) {
-        a.codes[i * a.ld + j] = code_of(v[e] * rs);
+        a.codes[i * a.ld + j] = code_of(by(v[e]));
         if (y_out) y_out[j] = from_f32<T>(v[e]);
       }
     }
@@ -440,9 +471,10 @@ __global__ void __launch_bounds__(kMaxThreads) norm_quant_long_kernel(NormQuantA
 
 // ---------------------------------------------------------------- weights
 // One CTA per block of 128 x 128, read once in pieces of 8, 16 lanes along a row (ANY: rows of any alignment
-// and width; else 16-byte aligned rows of whole pieces).  Every thread keeps what it read, as it was read, until the block's maximum is known.  Bound by memory: several CTAs share an SM so that one
-// block's loads run beside another's stores, and what a thread keeps decides how many.  bf16, 25152 x 4096
-// (309 MB) on a B200: 49 us, 6.3 TB/s, with three CTAs; 58 with two, 59 with four, which spill.
+// and width; else 16-byte aligned rows of whole pieces).  Every thread keeps what it read, as it was read,
+// until the block's maximum is known.  Bound by memory: several CTAs share an SM so that one block's loads run
+// beside another's stores, and what a thread keeps decides how many.  bf16, 25152 x 4096 (309 MB) on a B200:
+// 52 us, 5.9 TB/s, with three CTAs (which spill 4 bytes a thread); 61 with two, 55 with four (which spill 52).
 constexpr int kWeightThreads = 512;
 
 // Largest magnitude of the CTA's threads.
@@ -481,13 +513,14 @@ __global__ void __launch_bounds__(kWeightThreads, sizeof(T) == 2 ? 3 : 2)
     v[r].values(f);
     m = max_nan(m, piece_max(f));
   }
-  const float s = scale_of(block_max(m)), rs = 1.f / s;
+  const float s = scale_of(block_max(m));
+  const Quotient by(s);
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     if (row + r * STEP >= a.n || col >= a.k) continue;
     float f[kPiece];
     v[r].values(f);
-    store_codes<ANY>(a.codes + (row + r * STEP) * a.ld + col, codes_of(f, rs), a.k - col);
+    store_codes<ANY>(a.codes + (row + r * STEP) * a.ld + col, codes_of(f, by), a.k - col);
   }
   if (threadIdx.x == 0) a.scale[blockIdx.x] = s;
 }

@@ -188,3 +188,51 @@ def test_holders_allocate_what_the_calls_need():
     assert q.codes.shape == (5, 304) and q.scale.shape == (3, 8)
     w = qkn.Fp8Weight.empty(130, 300, "cpu")
     assert w.codes.shape == (130, 304) and w.scale.shape == (2, 3)
+
+
+# ---------------------------------------------------------------- the kernels' quotient
+def _fp32(x):
+    """An exact number rounded to 24 significant bits, ties to even (any exponent)."""
+    if x == 0:
+        return x
+    sign, x, e = (-1 if x < 0 else 1), abs(x), 0
+    while x >= 2:
+        x, e = x / 2, e + 1
+    while x < 1:
+        x, e = x * 2, e - 1
+    y = x * 2 ** 23
+    f = y.numerator // y.denominator
+    if y - f > Fraction(1, 2) or (y - f == Fraction(1, 2) and f % 2):
+        f += 1
+    return sign * Fraction(f) * Fraction(2) ** (e - 23)
+
+
+def test_corrected_quotient_gives_the_code_of_the_rounded_one():
+    """The kernels take v / s as q = v r with r = 1 / s, corrected by (v - q s) r.  q differs from v / s by at most
+    1.5 units of the last place, so the corrected value before its rounding by at most 2^-22 units, and its code is
+    that of the rounded quotient unless v / s lies that close to a border M -+ 2^-24 (M in [1, 2): the middle of two
+    codes, 5 significant bits) between the numbers that round to M and their neighbours.  With s = S 2^-23 and v on
+    its grid that is |S u - r| = 0 modulo 2^24 for u = M 2^24 -+ 1 and a small r: a few S for each u and r, all of
+    which are tried here, in exact arithmetic (64 times the bound's share of r)."""
+    cases = 0
+    for m in range(16, 32):
+        for side in (1, -1):
+            u = m * 2 ** 20 + side
+            inv = pow(u, -1, 2 ** 24)
+            for r in range(-64, 65):
+                S = r * inv % 2 ** 24
+                if S < 2 ** 23:
+                    continue
+                s = Fraction(S, 2 ** 23)
+                for bits in (23, 22):
+                    near = round(s * Fraction(u, 2 ** 24) * 2 ** bits)
+                    for v in (Fraction(near + i, 2 ** bits) for i in (-1, 0, 1)):
+                        if _fp32(v) != v:
+                            continue
+                        inverse = _fp32(1 / s)
+                        q = _fp32(v * inverse)
+                        q = _fp32(q + _fp32(v - q * s) * inverse)
+                        mid, want = Fraction(m, 16), _fp32(v / s)
+                        assert (q > mid) - (q < mid) == (want > mid) - (want < mid), (S, v, m)
+                        cases += 1
+    assert cases > 5000

@@ -451,3 +451,77 @@ def test_tensors_on_another_device_than_the_current_one():
     assert torch.equal(out.cpu(), want.cpu())
     with pytest.raises(ValueError):
         qkn.fp8_linear(a1, w, [out], workspace())
+
+
+# ---------------------------------------------------------------- codes to the bit
+def quotient_codes(y, scale):
+    """The codes of fp32 values on the host, by their definition: the fp32 quotient, rounded to the nearest e4m3."""
+    return (y.float() / scale).to(torch.float8_e4m3fn).float()
+
+
+def assert_codes(codes, y, scale):
+    got, want = codes.float().cpu(), quotient_codes(y.cpu(), scale.cpu())
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)), f"{(got != want).sum().item()} codes differ"
+
+
+def beside_midpoints(n, d, dtype, seed):
+    """Rows whose blocks hold, next to a random largest value, values in the middle between two codes and the
+    numbers of the type next to these, some zeros and tiny values, and ordinary ones."""
+    g = torch.Generator().manual_seed(seed)
+    grid = torch.from_numpy(oracle.e4m3_values())
+    mid = ((grid[1:] + grid[:-1]) / 2).float()
+    x = torch.randn((n, d), generator=g)
+    for i in range(n):
+        for j in range(0, d, 128):
+            row = x[i, j:j + 128]
+            top = (torch.rand((), generator=g) + 1) * 2.0 ** int(torch.randint(-40, 40, (), generator=g))
+            top = top.to(dtype).float()
+            v = mid[torch.randint(0, len(mid), (len(row),), generator=g)] * (top / 448)
+            step = torch.randint(-1, 2, (len(row),), generator=g, dtype=torch.int32)
+            bits = v.to(dtype).view(torch.int16 if dtype == torch.bfloat16 else torch.int32)
+            v = (bits + step.to(bits.dtype)).view(dtype).float()
+            pick = torch.rand(len(row), generator=g)
+            row.copy_(torch.where(pick < 0.8, v, torch.where(pick < 0.9, row * top / 4, torch.zeros(()))))
+            row.clamp_(-top, top)
+            row.mul_(torch.where(torch.rand(len(row), generator=g) < 0.5, -1.0, 1.0))
+            row[int(torch.randint(0, len(row), (), generator=g))] = top
+    return x.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,k", [(2, 8), (70, 512), (300, 333), (513, 1000)])
+def test_weight_codes_are_the_rounded_quotients(n, k, dtype):
+    for w in (torch.randn((n, k), generator=torch.Generator().manual_seed(n)).to(dtype),
+              beside_midpoints(n, k, dtype, n + k)):
+        q = qkn.Fp8Weight.empty(n, k)
+        qkn.quant_weight(w.cuda(), q)
+        per = np.array([[w[i:i + 128, j:j + 128].float().abs().max() for j in range(0, k, 128)] for i in range(0, n, 128)])
+        scale = torch.from_numpy(per) / 448
+        assert torch.equal(q.scale.cpu(), scale)
+        of = scale.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+        assert_codes(q.codes[:, :k], w, of)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,d", [(1, 8), (40, 512), (9, 5000), (33, 333), (1030, 264), (2, 20001), (2, 33000)])
+def test_row_codes_are_the_rounded_quotients(n, d, dtype):
+    """Without a norm from the values as they come; with one, in fp32, from the normalised rows that the call wrote."""
+    for x in (hidden(n, d, dtype, d), beside_midpoints(min(n, 40), d, dtype, n + d).cuda()):
+        m = x.shape[0]
+        q, _, _ = run_norm(x)
+        of = lambda q: q.scale[:, :m].t().repeat_interleave(128, 1)[:, :d]
+        assert_codes(q.codes[:, :d], x, of(q))
+        per = torch.stack([x[:, j:j + 128].float().abs().amax(1) for j in range(0, d, 128)])
+        assert torch.equal(q.scale[:, :m].cpu(), per.cpu() / 448)
+        if dtype == torch.float32:
+            q, _, y = run_norm(x, torch.ones(d, device="cuda"), want_y=True)
+            assert_codes(q.codes[:, :d], y, of(q))
+
+
+def test_finite_values_beside_an_infinity_have_zero_codes():
+    x = hidden(2, 256, torch.float32, 3)
+    x[0, 5], x[1, 200] = float("inf"), float("-inf")
+    q, _, _ = run_norm(x)
+    assert_codes(q.codes, x, q.scale[:, :2].t().repeat_interleave(128, 1))
+    assert torch.isnan(q.codes.float()).sum() == 2 and (q.codes.float()[0, :5] == 0).all()
