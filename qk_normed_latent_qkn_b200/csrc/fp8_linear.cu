@@ -43,10 +43,12 @@ __device__ __forceinline__ bool wide_ok(const OutCols& o) {
   return reinterpret_cast<uintptr_t>(o.out) % (E * sizeof(O)) == 0 && o.ld % E == 0 && o.begin % E == 0;
 }
 
-// A load that stays where it is written: the compiler would move an ordinary one down to its use.
-__device__ __forceinline__ float load_early(const float* p) {
+// A scale.  The kernel before this one may still be writing it when this one starts, so it is neither read
+// through the read-only path (which __ldg takes: what it reads must not change while the kernel runs) nor
+// moved: not above the wait for that kernel, nor, where it is asked for early, down to its use.
+__device__ __forceinline__ float load_scale(const float* p) {
   float v;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 
@@ -326,14 +328,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const float* sa = p.a_scale + min(m * kPairM + (int)rank * 128 + quad * 32 + lane, p.m - 1);
       const float* sw = p.w_scale + (int64_t)min((n * N + half * C::kCols) / kFp8Group, (p.n - 1) / kFp8Group) * blocks;
       const int b1 = blocks > 1 ? 1 : 0;
-      float s0 = __ldg(sa) * __ldg(sw), s1 = __ldg(sa + b1 * p.ld_as) * __ldg(sw + b1);
+      float s0 = load_scale(sa) * load_scale(sw), s1 = load_scale(sa + b1 * p.ld_as) * load_scale(sw + b1);
 #pragma unroll
       for (int i = 0; i < C::kCols; ++i) total[i] = 0.f;
       for (int b = 0; b < blocks; b += 2) {
         const int b2 = min(b + 2, blocks - 1), b3 = min(b + 3, blocks - 1);
-        const float a2 = load_early(sa + b2 * p.ld_as), w2 = load_early(sw + b2);
+        const float a2 = load_scale(sa + b2 * p.ld_as), w2 = load_scale(sw + b2);
         enter(s0);
-        const float a3 = load_early(sa + b3 * p.ld_as), w3 = load_early(sw + b3);
+        const float a3 = load_scale(sa + b3 * p.ld_as), w3 = load_scale(sw + b3);
         if (b + 1 < blocks) enter(s1);
         s0 = a2 * w2;
         s1 = a3 * w3;
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
     for (int i = 0; i < C::kPart; ++i) total[i] = 0.f;
     float sw_lane = 0.f;             // the weight's scales of 32 blocks, one per lane
     for (int b = b0; b < b1; ++b) {
-      if (((b - b0) & 31) == 0) sw_lane = __ldg(sw + min(b + lane, b1 - 1));
+      if (((b - b0) & 31) == 0) sw_lane = load_scale(sw + min(b + lane, b1 - 1));
       const float s = __shfl_sync(0xffffffffu, sw_lane, (b - b0) & 31);
       if (!mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) { ok = false; break; }
       tc_fence_after();

@@ -1,6 +1,7 @@
 """The 8-bit projections without a GPU: the oracle's pins, the argument checks of the C ABI and of the
 binding (nothing is launched)."""
 import ctypes
+import os
 from fractions import Fraction
 
 import numpy as np
@@ -236,3 +237,16 @@ def test_corrected_quotient_gives_the_code_of_the_rounded_one():
                         assert (q > mid) - (q < mid) == (want > mid) - (want < mid), (S, v, m)
                         cases += 1
     assert cases > 5000
+
+
+# ---------------------------------------------------------------- what a chained kernel may read how
+def test_no_read_only_loads_of_what_the_kernel_before_writes():
+    """The product and the quantisation start while the kernel before them still runs and take their inputs from it.
+    The read-only path (ld.global.nc, __ldg, __restrict__ on const pointers) is for data that nothing writes while
+    the kernel runs, the wait for its predecessor included; whether a stale line is hit cannot be tested on a GPU."""
+    csrc = os.path.join(os.path.dirname(qkn.__file__), "csrc")
+    for name in ("fp8_linear.cu", "quant.cu"):
+        with open(os.path.join(csrc, name)) as f:
+            code = "\n".join(line.split("//")[0] for line in f)
+        for form in ("global.nc", "__ldg", "__restrict__", "__ldcs", "__ldca"):
+            assert form not in code, (name, form)
