@@ -523,6 +523,29 @@ QKN_EXPORT qkn_status qkn_quant_weight(qkn_dtype dtype, const void* w, const qkn
 QKN_EXPORT qkn_status qkn_fp8_linear(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dtype out_dtype,
                       int32_t n_outs, const qkn_out_cols* outs, void* workspace, size_t ws_bytes, void* stream);
 
+/* The kernels of qkn_fp8_linear: tiles whose K a cluster splits (few tiles), pairs of CTAs on tiles of 256 rows x 128
+ * or 256 columns (many). */
+typedef enum {
+  QKN_LINEAR_AUTO = 0, QKN_LINEAR_SPLIT = 1, QKN_LINEAR_PAIR_128 = 2, QKN_LINEAR_PAIR_256 = 3
+} qkn_linear_kernel;
+
+/* Optional knobs of the product (pass NULL for defaults). */
+typedef struct {
+  int32_t kernel;          /* qkn_linear_kernel; default QKN_LINEAR_AUTO: the shortest by the library's estimate.  Every
+                              kernel takes every size; their results differ by the order of the sums. */
+  int64_t wait_limit;      /* bounded-wait limit in clock cycles for the mbarrier waits; 0 = default (~1 s) */
+  int32_t test_stop;       /* tests only: one role of every CTA gives up, as if a wait had run out: 1 the producer (of
+                              a pair's even CTA), 2 the producer of its odd CTA, 3 the warp that issues the MMAs, 4 a
+                              warp that reads the sums.  The others' waits then run out, QKN_ERR_TIMEOUT is recorded,
+                              what is in flight is waited for and tensor memory is freed.  0 in use. */
+  int32_t test_at;         /* the block of K (counted over a CTA's tiles) at which roles 1 to 3 give up */
+} qkn_linear_opts;
+
+/* qkn_fp8_linear with options. */
+QKN_EXPORT qkn_status qkn_fp8_linear_ex(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dtype out_dtype,
+                      int32_t n_outs, const qkn_out_cols* outs, void* workspace, size_t ws_bytes,
+                      const qkn_linear_opts* opts, void* stream);
+
 /* Synchronise `stream`, then read the workspace status word into *device_status
  * (a qkn_status value; QKN_OK if no kernel recorded an error).  The word is
  * sticky until qkn_workspace_init clears it. */

@@ -23,12 +23,13 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_BOUNDS = range(
 F32, BF16 = 0, 1
 AK_CACHE, AK_ONE = 0, 1
 KERNEL_AUTO, KERNEL_SIMT, KERNEL_TCGEN05 = 0, 1, 2
+LINEAR_AUTO, LINEAR_SPLIT, LINEAR_PAIR_128, LINEAR_PAIR_256 = 0, 1, 2, 3
 
 EXPORTED = ["qkn_append", "qkn_absorb_query", "qkn_decode_workspace_size", "qkn_workspace_init",
             "qkn_decode", "qkn_read_device_status", "qkn_decode_kernel_for", "qkn_status_string",
             "qkn_version", "qkn_decode_noalloc", "qkn_append_absorb", "qkn_key_gram", "qkn_decode_up",
             "qkn_merge_partials", "qkn_gqa_append", "qkn_gqa_workspace_size", "qkn_gqa_decode",
-            "qkn_norm_quant", "qkn_quant_weight", "qkn_fp8_linear"]
+            "qkn_norm_quant", "qkn_quant_weight", "qkn_fp8_linear", "qkn_fp8_linear_ex"]
 MAX_OUTS = 8               # destinations of one fp8_linear
 WORKSPACE_BYTES = 256      # what fp8_linear needs of a workspace (the status word)
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -71,6 +72,11 @@ class _OutCols(ctypes.Structure):
     _fields_ = [("out", ctypes.c_void_p), ("cols", ctypes.c_int32), ("ld", ctypes.c_int64)]
 
 
+class _LinearOpts(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("wait_limit", ctypes.c_int64), ("test_stop", ctypes.c_int32),
+                ("test_at", ctypes.c_int32)]
+
+
 class _Opts(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("max_ctas", ctypes.c_int32), ("head_tile", ctypes.c_int32),
                 ("wait_limit", ctypes.c_int64), ("split_event", ctypes.c_void_p),
@@ -107,6 +113,7 @@ def _load() -> ctypes.CDLL:
         "qkn_norm_quant": (I32, [I32, P, I64, P, P, ctypes.c_float, P, P, PR, P]),
         "qkn_quant_weight": (I32, [I32, P, PW, P]),
         "qkn_fp8_linear": (I32, [PR, PW, I32, I32, PU, P, SZ, P]),
+        "qkn_fp8_linear_ex": (I32, [PR, PW, I32, I32, PU, P, SZ, ctypes.POINTER(_LinearOpts), P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -483,9 +490,10 @@ def quant_weight(w, q: Fp8Weight, stream=None) -> None:
         raise QknError(status, "qkn_quant_weight")
 
 
-def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=None) -> None:
+def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=None, kernel: int = LINEAR_AUTO,
+               wait_limit: int = 0, test_stop: int = 0, test_at: int = 0) -> None:
     """out = A W^T from 8 bits (see qkn_fp8_linear); ``outs``: up to MAX_OUTS tensors [a.rows, width] of one type,
-    their rows contiguous, that take the product's columns in order."""
+    their rows contiguous, that take the product's columns in order.  The other arguments: see qkn_linear_opts."""
     n_outs, index, rows = len(outs), a.codes.get_device(), a.rows
     if not 1 <= n_outs <= MAX_OUTS:
         raise ValueError(f"outs holds 1 to {MAX_OUTS} tensors")
@@ -504,7 +512,11 @@ def fp8_linear(a: Fp8Rows, w: Fp8Weight, outs, workspace: torch.Tensor, stream=N
     if w.codes.get_device() != index or workspace.get_device() != index:
         raise ValueError("all tensors are on one device")
     ca, cw, ws, ws_bytes = ctypes.byref(a.c()), ctypes.byref(w.c()), workspace.data_ptr(), workspace.nbytes
-    if stream is None and index >= 0 and index == _cuda_device():
+    if kernel or wait_limit or test_stop:
+        opts = _LinearOpts(kernel, wait_limit, test_stop, test_at)
+        status = _call_on(index, stream, rows, _lib.qkn_fp8_linear_ex, ca, cw, dtype, n_outs, arr, ws, ws_bytes,
+                          ctypes.byref(opts))
+    elif stream is None and index >= 0 and index == _cuda_device():
         status = _lib.qkn_fp8_linear(ca, cw, dtype, n_outs, arr, ws, ws_bytes, _cuda_stream(index))
     else:
         status = _call_on(index, stream, rows, _lib.qkn_fp8_linear, ca, cw, dtype, n_outs, arr, ws, ws_bytes)

@@ -745,12 +745,21 @@ qkn_status qkn_quant_weight(qkn_dtype dtype, const void* w, const qkn_fp8_weight
 
 qkn_status qkn_fp8_linear(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dtype out_dtype, int32_t n_outs,
                           const qkn_out_cols* outs, void* workspace, size_t ws_bytes, void* stream) {
+  return qkn_fp8_linear_ex(a, w, out_dtype, n_outs, outs, workspace, ws_bytes, nullptr, stream);
+}
+
+qkn_status qkn_fp8_linear_ex(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dtype out_dtype, int32_t n_outs,
+                             const qkn_out_cols* outs, void* workspace, size_t ws_bytes, const qkn_linear_opts* opts,
+                             void* stream) {
   if (!check_dtype(out_dtype) || !a || !w || !outs || n_outs < 1 || n_outs > QKN_MAX_OUTS) return QKN_ERR_INVALID_ARG;
   if (a->ld_scale < 4 || !check_fp8(a->codes, a->scale, a->rows, a->cols, a->ld, a->ld_scale) ||
       !check_fp8(w->codes, w->scale, w->rows, w->cols, w->ld, 0))
     return QKN_ERR_INVALID_ARG;
   if (w->rows < 1 || a->cols != w->cols) return QKN_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256) || ws_bytes < (size_t)kStatusBytes) return QKN_ERR_INVALID_ARG;
+  if (opts && (opts->kernel < QKN_LINEAR_AUTO || opts->kernel > QKN_LINEAR_PAIR_256 || opts->wait_limit < 0 ||
+               opts->test_stop < 0 || opts->test_stop > 4 || opts->test_at < 0 || opts->test_at > (1 << 30)))
+    return QKN_ERR_INVALID_ARG;
   Fp8LinearArgs l;
   int64_t at = 0;
   for (int i = 0; i < n_outs; ++i) {
@@ -773,6 +782,10 @@ qkn_status qkn_fp8_linear(const qkn_fp8_rows* a, const qkn_fp8_weight* w, qkn_dt
   l.k = a->cols;
   l.n_outs = n_outs;
   l.status = static_cast<int32_t*>(workspace);
+  l.wait_limit = opts && opts->wait_limit > 0 ? opts->wait_limit : kLinearWaitCycles;
+  l.kernel = opts ? opts->kernel : QKN_LINEAR_AUTO;
+  l.test_stop = opts ? opts->test_stop : 0;
+  l.test_at = opts ? opts->test_at : 0;
   cudaError_t err = launch_fp8_linear(l, out_dtype == QKN_BF16, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? QKN_OK : QKN_ERR_CUDA;
 }

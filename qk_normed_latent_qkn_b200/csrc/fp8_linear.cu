@@ -31,7 +31,6 @@ struct LinearMaps {
 
 namespace {
 
-constexpr int64_t kWaitCycles = 2000000000LL;   // about a second: any wait that long is a fault
 constexpr int kRowBytes = 128;                  // codes of one block of K in a tile row
 constexpr int kTileBytes = 128 * kRowBytes;     // 128 rows of a tile
 constexpr int kKStep = 32;                      // K of one MMA
@@ -48,7 +47,7 @@ __device__ __forceinline__ bool wide_ok(const OutCols& o) {
 // moved: not above the wait for that kernel, nor, where it is asked for early, down to its use.
 __device__ __forceinline__ float load_scale(const float* p) {
   float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
 
@@ -171,9 +170,18 @@ template <int S, int A>
 struct PairBars {
   uint64_t full[S], empty[S];
   uint64_t t_full[A], t_empty[A];
-  uint64_t drained;                             // used once a wait has run out: the MMAs in flight are done
   uint32_t tmem;
+  // For the way out after a wait that ran out, in both CTAs of the pair alike: whether one did, the blocks
+  // that each CTA's producer asked for, and the blocks that went to the tensor core.
+  uint32_t failed, issued[2], computed;
 };
+
+// Waits for the last uses, up to `uses`, of a ring of n mbarriers.  (A call: the loops that are never gone
+// through stay out of the kernels' registers.)
+__device__ __noinline__ void wait_last(uint32_t bars, int n, int uses) {
+  for (int u = uses > n ? uses - n : 0; u < uses; ++u)
+    (void)mbar_wait_warp(bars + (uint32_t)(u % n) * 8, (uint32_t)(u / n) & 1u, kLinearWaitCycles);
+}
 
 template <int N>
 struct TileWalk {
@@ -191,7 +199,7 @@ struct TileWalk {
 
 // Warps: 0 producer, 1 MMA (the even CTA issues for both), 2-9 epilogue (each CTA its 128 rows; warps
 // 2-5 the first half of the tile's columns, 6-9 the second).
-template <int N, typename O>
+template <int N, typename O, bool STOP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ Fp8LinearArgs p, const __grid_constant__ LinearMaps maps) {
   using C = PairCfg<N>;
@@ -212,7 +220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       mbar_init(smem_u32(&bars.t_full[i]), 1);
       mbar_init(smem_u32(&bars.t_empty[i]), 2 * kPairWarps);   // of both CTAs
     }
-    mbar_init(smem_u32(&bars.drained), 1);
+    bars.failed = bars.issued[0] = bars.issued[1] = bars.computed = 0;
     mbar_fence_init();
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.w);
@@ -235,14 +243,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int pairs = gridDim.x >> 1;
   bool ok = true;
 
+  const auto tell = [&](uint32_t& word, uint32_t v) {   // both CTAs (the cluster barrier below orders it)
+    for (uint32_t r = 0; r < 2; ++r) st_shared_remote_u32(mapa_shared(smem_u32(&word), r), v);
+  };
+
   if (warp == 0) {
+    const int stop = STOP && p.test_stop == 1 + (int)rank ? p.test_at : INT32_MAX;
     RingPos<C::kStages> ring;
+    int uses = 0;
     for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
       int m, n;
       walk.of(t, m, n);
       const int y_a = m * kPairM + (int)rank * 128, y_w = n * N + (int)rank * (N / 2);
-      for (int b = 0; b < blocks; ++b) {
-        if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
+      int b = 0;
+      for (const int to = min(blocks, stop - uses); b < to; ++b) {
+        if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, p.wait_limit)) break;
         const uint32_t full = smem_u32(&bars.full[ring.slot]);
         if (rank == 0) mbar_arrive_expect_tx_elect(full, 2 * C::kStageBytes);
         const uint32_t dst = stages + ring.slot * C::kStageBytes;
@@ -251,26 +266,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         tma_load_2d_pair_elect(dst + kTileBytes, &maps.w, b * kFp8Group, y_w, bar);
         ring.next();
       }
+      uses += b;
+      ok = b == blocks;
     }
-    // the last uses of the stages end before this CTA does: their commits arrive here (after a wait that ran
-    // out, what this pair's copies still bring; the even CTA waits, the odd one for it)
+    // the last uses of the stages end before this CTA does: their commits arrive here
     for (int i = 0; i < C::kStages; ++i) {
-      if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
-      if (!ok && rank == 0) (void)mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase ^ 1u, kWaitCycles);
+      if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, p.wait_limit)) ok = false;
       ring.next();
     }
+    if (lane == 0) tell(bars.issued[rank], uses);
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t idesc = idesc_e4m3(256, N);
     const uint64_t d_a = smem_desc(stages, 16, 1024), d_w = smem_desc(stages + kTileBytes, 16, 1024);
+    const int stop = STOP && p.test_stop == 3 ? p.test_at : INT32_MAX;
     RingPos<C::kStages> ring;
     RingPos<C::kAccs> acc;
-    for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs)
-      for (int b = 0; b < blocks; ++b) {
-        if (!mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles) ||
-            !mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles)) {
-          ok = false;
+    int uses = 0;
+    for (int t = blockIdx.x >> 1; ok && t < tiles; t += pairs) {
+      int b = 0;
+      for (const int to = min(blocks, stop - uses); b < to; ++b) {
+        if (!mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, p.wait_limit) ||
+            !mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, p.wait_limit))
           break;
-        }
         tc_fence_after();
         const uint64_t at = (uint64_t)((ring.slot * C::kStageBytes) >> 4);
 #pragma unroll
@@ -282,21 +299,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         ring.next();
         acc.next();
       }
-    if (!ok) {
-      mma_commit_group2_elect(smem_u32(&bars.drained), 1);
-      (void)mbar_wait_warp(smem_u32(&bars.drained), 0, kWaitCycles);
+      uses += b;
+      ok = b == blocks;
     }
+    if (lane == 0) tell(bars.computed, uses);
   } else if (warp >= 2) {
     const int quad = warp & 3, half = (warp - 2) >> 2;
     uint8_t* box = smem + C::kBoxOff + (warp - 2) * kBoxBytes;
     const uint32_t tq = tmem + ((uint32_t)(quad * 32) << 16) + half * C::kCols;
+    if (STOP && p.test_stop == 4 && warp == 2) ok = false;
     RingPos<C::kAccs> acc;
     float total[C::kCols];
     // One block of K: its sums leave TMEM 16 columns at a time, the next ones on their way while these
     // enter the total.  (Single FMAs: as packed pairs they need the same FMA cycles and, with the moves
     // that pair up registers, more instructions.)
     auto enter = [&](float s) {
-      if (ok && !mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) ok = false;
+      if (ok && !mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, p.wait_limit)) ok = false;
       tc_fence_after();
       const uint32_t at = tq + acc.slot * N;
       constexpr int L = C::kCols / kLoadCols;
@@ -353,9 +371,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   }
   __syncwarp();
-  if (!ok && lane == 0) record_status(p.status, QKN_ERR_TIMEOUT);
+  if (!ok && lane == 0) {
+    record_status(p.status, QKN_ERR_TIMEOUT);
+    tell(bars.failed, 1);
+  }
+  __syncwarp();
   tc_fence_before();
   cluster_sync();
+  if (__builtin_expect(bars.failed, 0)) {
+    // A role gave up, and the others after it, at blocks of their own.  Nothing may be in flight when a CTA
+    // leaves.  First the MMAs, and with them their arrivals in both CTAs.  Then the copies: all of a block's
+    // complete on the even CTA's mbarrier, which was told to expect both CTAs' bytes, so a block that one CTA
+    // has asked for and the other has not would never be complete.  The other asks for it now.  (A producer
+    // that asked for a block had seen its stage's last use end, so that use's copies have arrived in both
+    // CTAs, the two are at most a ring apart, and no MMA reads the stage any more.  Which bytes come is
+    // all the same; the same tile corner is in bounds, or zeros.)
+    if (warp == 0) {
+      wait_last(smem_u32(bars.empty), C::kStages, bars.computed);
+      wait_last(smem_u32(bars.t_full), C::kAccs, bars.computed);
+    }
+    cluster_sync();
+    if (warp == 0) {
+      const int uses = max(bars.issued[0], bars.issued[1]);
+      for (int u = bars.issued[rank]; u < uses; ++u) {
+        const int slot = u % C::kStages;
+        const uint32_t full = smem_u32(&bars.full[slot]), dst = stages + slot * C::kStageBytes;
+        if (rank == 0) mbar_arrive_expect_tx_elect(full, 2 * C::kStageBytes);
+        tma_load_2d_pair_elect(dst, &maps.a, 0, 0, mapa_shared(full, 0));
+        tma_load_2d_pair_elect(dst + kTileBytes, &maps.w, 0, 0, mapa_shared(full, 0));
+      }
+      if (rank == 0) wait_last(smem_u32(bars.full), C::kStages, uses);
+    }
+    cluster_sync();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
@@ -371,6 +419,9 @@ struct SplitCfg {
   static constexpr int kPitch = kRows ? 132 : 128;                       // floats of a row of partial sums
   static constexpr int kThreads = 64 + 32 * kWarps;                       // (and the producer, the MMA)
   static constexpr int kPerSm = NT == 128 ? 1 : 2;                       // CTAs on an SM (registers, shared memory)
+  // CTAs that the registers are shared out for; 64 rows are faster without (19.2 us for 18.4 at 64 x 4096 x 16384),
+  // the others with (32 x 25152 x 4096: 21.2 for 22.3; 128 x 4096 x 16384: 18.1 for 19.6)
+  static constexpr int kBound = NT == 64 ? 0 : kPerSm;
   static constexpr int kStageBytes = kTileBytes + NT * kRowBytes;         // weight, rows
   static constexpr int kStages = NT == 128 ? 6 : NT == 64 ? 4 : 5;
   static constexpr int kCols = NT < 32 ? 32 : NT;                        // TMEM columns of one accumulator
@@ -394,8 +445,8 @@ template <int S, int A>
 struct SplitBars {
   uint64_t full[S], empty[S];
   uint64_t t_full[A], t_empty[A];
-  uint64_t drained;   // as in PairBars
   uint32_t tmem;
+  uint32_t failed, issued, computed;   // as in PairBars
 };
 
 // Bound by memory or, in short calls, by the chain of one load, MMA, promotion and join: 32 x 25152 x 4096
@@ -404,10 +455,10 @@ struct SplitBars {
 // added in rank order: the same bits every time.
 // One tile: 128 columns of the product for NT rows.  Cluster rank r takes the r-th part of K's blocks.
 // Warps: 0 producer, 1 MMA, 2 on: epilogue.
-template <int NT, typename O>
-__global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(const __grid_constant__ Fp8LinearArgs p,
-                                                           const __grid_constant__ LinearMaps maps, int split,
-                                                           int row_tiles) {
+template <int NT, typename O, bool STOP>
+__global__ void __launch_bounds__(SplitCfg<NT>::kThreads, SplitCfg<NT>::kBound)
+    linear_split_kernel(const __grid_constant__ Fp8LinearArgs p, const __grid_constant__ LinearMaps maps, int split,
+                        int row_tiles) {
   using C = SplitCfg<NT>;
   extern __shared__ __align__(16) uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
@@ -431,7 +482,7 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
       mbar_init(smem_u32(&bars.t_full[i]), 2);             // the MMA warp, and its MMAs when they are done
       mbar_init(smem_u32(&bars.t_empty[i]), C::kWarps);
     }
-    mbar_init(smem_u32(&bars.drained), 1);
+    bars.failed = 0;
     mbar_fence_init();
     prefetch_tmap(&maps.a);
     prefetch_tmap(&maps.w);
@@ -448,13 +499,13 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
   pdl_trigger();
   pdl_wait();
 
-  bool ok = true;
   float total[C::kPart];
   if (warp == 0) {
     RingPos<C::kStages> ring;
     RingPos<C::kScaleSlots> sring;
-    for (int b = b0; b < b1; ++b) {
-      if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) { ok = false; break; }
+    int b = b0;
+    for (const int to = STOP && (p.test_stop == 1 || p.test_stop == 2) ? min(b1, b0 + p.test_at) : b1; b < to; ++b) {
+      if (!mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, p.wait_limit)) break;
       const uint32_t full = smem_u32(&bars.full[ring.slot]);
       const uint32_t dst = stages + ring.slot * C::kStageBytes;
       mbar_arrive_expect_tx_elect(full, C::kStageBytes + NT * 4);
@@ -464,23 +515,24 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
       ring.next();
       sring.next();
     }
-    for (int i = 0; i < C::kStages; ++i) {                  // nothing of this CTA's is in flight after this
-      if (ok && !mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, kWaitCycles)) ok = false;
-      if (!ok) (void)mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase ^ 1u, kWaitCycles);
+    if (lane == 0) bars.issued = b - b0;
+    bool ok = b == b1;
+    for (int i = 0; ok && i < C::kStages; ++i) {            // nothing of this CTA's is in flight after this
+      ok = mbar_wait_warp(smem_u32(&bars.empty[ring.slot]), ring.phase ^ 1u, p.wait_limit);
       ring.next();
     }
+    if (!ok && lane == 0) bars.failed = 1;
   } else if (warp == 1) {
     constexpr uint32_t idesc = idesc_e4m3(128, NT);
     const uint64_t d_w = smem_desc(stages, 16, 1024), d_a = smem_desc(stages + kTileBytes, 16, 1024);
     const uint64_t d_m = C::kRows ? d_a : d_w, d_n = C::kRows ? d_w : d_a;
     RingPos<C::kStages> ring;
     RingPos<C::kAccs> acc;
-    for (int b = b0; b < b1; ++b) {
-      if (!mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, kWaitCycles) ||
-          !mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, kWaitCycles)) {
-        ok = false;
+    int b = b0;
+    for (const int to = STOP && p.test_stop == 3 ? min(b1, b0 + p.test_at) : b1; b < to; ++b) {
+      if (!mbar_wait_warp(smem_u32(&bars.t_empty[acc.slot]), acc.phase ^ 1u, p.wait_limit) ||
+          !mbar_wait_warp(smem_u32(&bars.full[ring.slot]), ring.phase, p.wait_limit))
         break;
-      }
       tc_fence_after();
       const uint64_t at = (uint64_t)((ring.slot * C::kStageBytes) >> 4);
 #pragma unroll
@@ -492,10 +544,8 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
       ring.next();
       acc.next();
     }
-    if (!ok) {
-      mma_commit_elect(smem_u32(&bars.drained));
-      (void)mbar_wait_warp(smem_u32(&bars.drained), 0, kWaitCycles);
-    }
+    if (lane == 0) bars.computed = b - b0;
+    if (b < b1 && lane == 0) bars.failed = 1;
   } else {
     const int quad = warp & 3, part = (warp - 2) >> 2;
     const float* sw = p.w_scale + (int64_t)(n0 / kFp8Group) * blocks;
@@ -504,10 +554,11 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
 #pragma unroll
     for (int i = 0; i < C::kPart; ++i) total[i] = 0.f;
     float sw_lane = 0.f;             // the weight's scales of 32 blocks, one per lane
-    for (int b = b0; b < b1; ++b) {
+    int b = b0;
+    for (const int to = STOP && p.test_stop == 4 && warp == 2 ? b0 : b1; b < to; ++b) {
       if (((b - b0) & 31) == 0) sw_lane = load_scale(sw + min(b + lane, b1 - 1));
       const float s = __shfl_sync(0xffffffffu, sw_lane, (b - b0) & 31);
-      if (!mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, kWaitCycles)) { ok = false; break; }
+      if (!mbar_wait_warp(smem_u32(&bars.t_full[acc.slot]), acc.phase, p.wait_limit)) break;
       tc_fence_after();
       const uint8_t* sa = smem + C::kScaleOff + sring.slot * C::kScaleBytes;
       const uint32_t at = tmem + ((uint32_t)(quad * 32) << 16) + acc.slot * C::kCols + part * C::kPart;
@@ -539,11 +590,22 @@ __global__ void __launch_bounds__(SplitCfg<NT>::kThreads) linear_split_kernel(co
       sring.next();
       acc.next();
     }
+    if (b < b1 && lane == 0) bars.failed = 1;
   }
   __syncwarp();
-  if (!ok && lane == 0) record_status(p.status, QKN_ERR_TIMEOUT);
   tc_fence_before();
-  __syncthreads();                                          // every stage is free: the partial sums take their place
+  __syncthreads();
+  // every stage is free, and the partial sums take their place; after a wait that ran out, once the copies and
+  // MMAs in flight have ended
+  if (__builtin_expect(bars.failed, 0)) {
+    if (threadIdx.x == 0) record_status(p.status, QKN_ERR_TIMEOUT);
+    if (warp == 0) {
+      wait_last(smem_u32(bars.full), C::kStages, bars.issued);
+      wait_last(smem_u32(bars.empty), C::kStages, bars.computed);
+      wait_last(smem_u32(bars.t_full), C::kAccs, bars.computed);
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols * C::kAccs);
@@ -632,21 +694,27 @@ bool codes_map(CUtensorMap* m, const uint8_t* codes, int k, int rows, int64_t ld
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-template <int N, typename O>
-cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
+template <int N, typename O, bool STOP>
+cudaError_t launch_pair_as(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
   LinearMaps maps;
   if (!codes_map(&maps.a, a.a, a.k, a.m, a.lda, 128) || !codes_map(&maps.w, a.w, a.k, a.n, a.ldw, N / 2))
     return cudaErrorInvalidValue;
   static PerDeviceOnce attrs;
   cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(linear_pair_kernel<N, O>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(linear_pair_kernel<N, O, STOP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 PairCfg<N>::kSmem);
   });
   if (e != cudaSuccess) return e;
   const int64_t tiles = (int64_t)ceil_div(a.m, kPairM) * ceil_div(a.n, N);
   if (tiles > (1 << 30)) return cudaErrorInvalidConfiguration;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_chained(linear_pair_kernel<N, O>, dim3(2 * pairs), dim3(kPairThreads), PairCfg<N>::kSmem, st, a, maps);
+  return launch_chained(linear_pair_kernel<N, O, STOP>, dim3(2 * pairs), dim3(kPairThreads), PairCfg<N>::kSmem, st, a, maps);
+}
+
+// (The instances with STOP are for tests; what they add to the loops would cost up to a twentieth.)
+template <int N, typename O>
+cudaError_t launch_pair(const Fp8LinearArgs& a, int sms, cudaStream_t st) {
+  return a.test_stop ? launch_pair_as<N, O, true>(a, sms, st) : launch_pair_as<N, O, false>(a, sms, st);
 }
 
 // Clusters of `size` CTAs that the device holds at once, one CTA per SM: fewer than its SMs' worth, because a
@@ -665,7 +733,7 @@ int clusters_of(int size, int sms) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<NT, O>, &cfg) != cudaSuccess || n < 1) {
+  if (cudaOccupancyMaxActiveClusters(&n, linear_split_kernel<NT, O, false>, &cfg) != cudaSuccess || n < 1) {
     (void)cudaGetLastError();
     n = 1;
   }
@@ -697,10 +765,10 @@ int split_of(int64_t tiles, int blocks, int dev, int sms) {
   return split;
 }
 
-template <int NT, typename O>
+template <int NT, typename O, bool STOP = false>
 cudaError_t split_attrs() {
   static PerDeviceOnce attrs;
-  return once_per_device(attrs, [] { return set_smem_attrs(linear_split_kernel<NT, O>, SplitCfg<NT>::kSmem); });
+  return once_per_device(attrs, [] { return set_smem_attrs(linear_split_kernel<NT, O, STOP>, SplitCfg<NT>::kSmem); });
 }
 
 template <int NT, typename O>
@@ -731,7 +799,12 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int dev, int sms, cudaStream_t 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, O>, a, maps, split, row_tiles);
+  if (a.test_stop) {
+    const cudaError_t t = split_attrs<NT, O, true>();
+    if (t != cudaSuccess) return t;
+    return cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, O, true>, a, maps, split, row_tiles);
+  }
+  return cudaLaunchKernelEx(&cfg, linear_split_kernel<NT, O, false>, a, maps, split, row_tiles);
 }
 
 // Which kernel takes more than 64 rows.  All three walk their tiles in waves over the SMs; the constants
@@ -746,18 +819,16 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int dev, int sms, cudaStream_t 
 //   2048 x  576 x 4096            20             15         18
 //   333 x  1000 x 1960            16             10         7.5
 //   4096 x 4096 x 16384          303            374          -
-enum class Kernel { kPair256, kPair128, kSplit };
-
 template <typename O>
-Kernel choose(int64_t m, int64_t n, int blocks, int dev, int sms) {
+int choose(int64_t m, int64_t n, int blocks, int dev, int sms) {
   const int64_t row_tiles = ceil_div(m, kPairM);
   const int64_t wide = 4000 + ceil_div(row_tiles * ceil_div(n, 256), sms / 2) * (1500 + (int64_t)blocks * 480);
   const int64_t narrow = 4000 + ceil_div(row_tiles * ceil_div(n, 128), sms / 2) * (1500 + (int64_t)blocks * 335);
   const int64_t tiles = (int64_t)ceil_div(m, 128) * ceil_div(n, 128);
   const int parts = split_of<128, O>(tiles, blocks, dev, sms);
   const int64_t split = ceil_div(tiles * parts, sms) * (5000 + (int64_t)ceil_div(blocks, parts) * 380);
-  if (split <= wide && split <= narrow) return Kernel::kSplit;
-  return narrow < wide ? Kernel::kPair128 : Kernel::kPair256;
+  if (split <= wide && split <= narrow) return QKN_LINEAR_SPLIT;
+  return narrow < wide ? QKN_LINEAR_PAIR_128 : QKN_LINEAR_PAIR_256;
 }
 
 template <typename O>
@@ -766,14 +837,17 @@ cudaError_t launch(const Fp8LinearArgs& a, cudaStream_t st) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  if (a.m > 64) {
-    if ((e = split_attrs<128, O>()) != cudaSuccess) return e;   // (the estimate asks for the kernel's occupancy)
-    switch (choose<O>(a.m, a.n, ceil_div(a.k, kFp8Group), dev, sms)) {
-      case Kernel::kPair256: return launch_pair<256, O>(a, sms, st);
-      case Kernel::kPair128: return launch_pair<128, O>(a, sms, st);
-      case Kernel::kSplit: return launch_split<128, O>(a, dev, sms, st);
+  int kernel = a.kernel;
+  if (kernel == QKN_LINEAR_AUTO) {
+    kernel = QKN_LINEAR_SPLIT;
+    if (a.m > 64) {
+      if ((e = split_attrs<128, O>()) != cudaSuccess) return e;   // (the estimate asks for the kernel's occupancy)
+      kernel = choose<O>(a.m, a.n, ceil_div(a.k, kFp8Group), dev, sms);
     }
   }
+  if (kernel == QKN_LINEAR_PAIR_256) return launch_pair<256, O>(a, sms, st);
+  if (kernel == QKN_LINEAR_PAIR_128) return launch_pair<128, O>(a, sms, st);
+  if (a.m > 64) return launch_split<128, O>(a, dev, sms, st);
   // the smallest of 16, 32 and 64 rows that holds them all: every tile reads its weight rows once
   if (a.m > 32) return launch_split<64, O>(a, dev, sms, st);
   if (a.m > 16) return launch_split<32, O>(a, dev, sms, st);

@@ -211,7 +211,12 @@ struct Fp8LinearArgs {
   int32_t n_outs;
   OutCols outs[QKN_MAX_OUTS];
   int32_t* status;         // workspace status word
+  int64_t wait_limit;      // of a wait on an mbarrier, in clock cycles
+  int32_t kernel;          // qkn_linear_kernel
+  int32_t test_stop, test_at;   // qkn_linear_opts
 };
+
+constexpr int64_t kLinearWaitCycles = 2000000000LL;   // about a second: any wait that long is a fault
 
 cudaError_t launch_norm_quant(const NormQuantArgs& a, bool bf16, cudaStream_t st);
 cudaError_t launch_quant_weight(const QuantWeightArgs& a, bool bf16, cudaStream_t st);

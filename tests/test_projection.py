@@ -250,3 +250,16 @@ def test_no_read_only_loads_of_what_the_kernel_before_writes():
             code = "\n".join(line.split("//")[0] for line in f)
         for form in ("global.nc", "__ldg", "__restrict__", "__ldcs", "__ldca"):
             assert form not in code, (name, form)
+
+
+# ---------------------------------------------------------------- options of the product
+@pytest.mark.parametrize("opts", [dict(kernel=-1), dict(kernel=4), dict(wait_limit=-1), dict(test_stop=-1),
+                                  dict(test_stop=5), dict(test_stop=1, test_at=-1)])
+def test_fp8_linear_refuses_bad_options(opts):
+    arr = (qkn._OutCols * 1)(qkn._OutCols(P, 64, 64))
+    call = lambda o: qkn.raw_library().qkn_fp8_linear_ex(ctypes.byref(_rows()), ctypes.byref(_weight()), qkn.BF16, 1,
+                                                         arr, P, 256, ctypes.byref(o), None)
+    assert call(qkn._LinearOpts(**opts)) == qkn.ERR_INVALID_ARG
+    rows = _rows(rows=0, codes=None, scale=None)
+    assert qkn.raw_library().qkn_fp8_linear_ex(ctypes.byref(rows), ctypes.byref(_weight()), qkn.BF16, 1, arr, P, 256,
+                                               ctypes.byref(qkn._LinearOpts(kernel=3)), None) == qkn.OK

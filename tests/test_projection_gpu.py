@@ -525,3 +525,34 @@ def test_finite_values_beside_an_infinity_have_zero_codes():
     q, _, _ = run_norm(x)
     assert_codes(q.codes, x, q.scale[:, :2].t().repeat_interleave(128, 1))
     assert torch.isnan(q.codes.float()).sum() == 2 and (q.codes.float()[0, :5] == 0).all()
+
+
+# ---------------------------------------------------------------- waits that run out
+SHORT_WAIT = 1_000_000      # about half a millisecond
+
+
+@pytest.mark.parametrize("stop", [1, 2, 3, 4])
+@pytest.mark.parametrize("kernel,m,n,k,ats", [
+    (qkn.LINEAR_SPLIT, 3, 700, 4096, (0, 1, 3)), (qkn.LINEAR_SPLIT, 30, 300, 2500, (0, 1)),
+    (qkn.LINEAR_SPLIT, 64, 9000, 1500, (0, 1)), (qkn.LINEAR_SPLIT, 333, 1000, 5000, (0, 7)),
+    (qkn.LINEAR_PAIR_128, 300, 500, 2000, (0, 3, 15)), (qkn.LINEAR_PAIR_128, 2049, 5000, 300, (0, 4)),
+    (qkn.LINEAR_PAIR_256, 300, 500, 2000, (0, 3, 15)), (qkn.LINEAR_PAIR_256, 2049, 5000, 300, (0, 4)),
+])
+def test_wait_that_runs_out_is_reported_and_the_next_product_is_correct(kernel, m, n, k, ats, stop):
+    """A role of every CTA gives up; the call records it and winds down, and the next one is right."""
+    a, w = operands(m, n, k, seed=11)
+    ws = workspace()
+    want = torch.empty((m, n), dtype=torch.float32, device="cuda")
+    qkn.fp8_linear(a, w, [want], ws, kernel=kernel)
+    torch.cuda.synchronize()
+    assert qkn.read_device_status(ws) == qkn.OK
+    out = torch.empty_like(want)
+    for at in ats if stop < 4 else ats[:1]:
+        qkn.fp8_linear(a, w, [out], ws, kernel=kernel, wait_limit=SHORT_WAIT, test_stop=stop, test_at=at)
+        assert qkn.read_device_status(ws) == qkn.ERR_TIMEOUT
+        qkn.workspace_init(ws)
+        out.fill_(float("nan"))
+        qkn.fp8_linear(a, w, [out], ws, kernel=kernel)
+        torch.cuda.synchronize()
+        assert qkn.read_device_status(ws) == qkn.OK
+        assert torch.equal(out, want)
