@@ -556,3 +556,76 @@ def test_wait_that_runs_out_is_reported_and_the_next_product_is_correct(kernel, 
         torch.cuda.synchronize()
         assert qkn.read_device_status(ws) == qkn.OK
         assert torch.equal(out, want)
+
+
+# ---------------------------------------------------------------- every kernel by name
+KERNELS = [qkn.LINEAR_SPLIT, qkn.LINEAR_PAIR_128, qkn.LINEAR_PAIR_256]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (5, 130, 300), (70, 1029, 128), (257, 520, 400), (300, 1400, 1100),
+                                   (1030, 2600, 260)])
+def test_every_kernel_writes_odd_places_and_nothing_else(m, n, k, kernel, dtype):
+    """Slices of wider buffers at odd places, widths that end inside a tile or a box, in every kernel: right values,
+    and what lies around stays."""
+    a, w = operands(m, n, k, seed=m + n, pad=48)
+    ref, mag = product(a, w)
+    for off, cuts in ((0, []), (1, []), (3, [8, n - 3]), (8, [n // 2]), (5, [n // 3, n // 2 + 1]), (2, [n - 1])):
+        cuts = sorted({0, n, *(c for c in cuts if 0 < c < n)})
+        widths = [q - p for p, q in zip(cuts, cuts[1:])]
+        bufs = [torch.full((m, c + 16), 5.0, dtype=dtype, device="cuda") for c in widths]
+        ws = workspace()
+        qkn.fp8_linear(a, w, [b[:, off:off + c] for b, c in zip(bufs, widths)], ws, kernel=kernel)
+        assert qkn.read_device_status(ws) == qkn.OK
+        got = np.concatenate([host(b[:, off:off + c]) for b, c in zip(bufs, widths)], axis=1)
+        check_product(got, ref, mag, k, dtype)
+        for b, c in zip(bufs, widths):
+            assert (b[:, :off] == 5.0).all() and (b[:, off + c:] == 5.0).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("m,n,k", [(3, 700, 1000), (300, 520, 640), (1500, 2560, 384)])
+def test_every_kernel_repeats_bit_for_bit_and_keeps_nan_in_its_row(m, n, k, kernel):
+    a, w = operands(m, n, k, seed=2)
+    a.scale[1, 1] = float("nan")
+    a.codes.view(torch.uint8)[2, 7] = 0x7F              # a code that is NaN
+    outs = [torch.empty((m, n), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    ws = workspace()
+    for o in outs:
+        qkn.fp8_linear(a, w, [o], ws, kernel=kernel)
+    bits = [o.view(torch.int16) for o in outs]
+    assert torch.equal(bits[0], bits[1]) and torch.equal(bits[0], bits[2])
+    assert torch.isnan(outs[0][1:3]).all() and torch.isfinite(outs[0][0]).all() and torch.isfinite(outs[0][3:]).all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("m", [40, 600])
+def test_every_kernel_in_a_chain_through_rewritten_buffers(m, kernel):
+    """As test_one_buffer_rewritten_between_back_to_back_products, with the kernel given and the weight rewritten by
+    every pair: its scales and codes come from the kernel before the last, the rows' from the last."""
+    n, k, rounds = 1300, 900, 12
+    xs = [hidden(m, k, torch.bfloat16, s) * 2.0 ** (s % 5) for s in range(rounds)]
+    ww = [(torch.randn((n, k), generator=torch.Generator().manual_seed(s)) * 2.0 ** (s % 3)).cuda() for s in range(3)]
+    ws = workspace()
+
+    def chain(sync):
+        q, w = qkn.Fp8Rows.empty(m, k), qkn.Fp8Weight.empty(n, k)
+        outs = [torch.empty((m, n), dtype=torch.float32, device="cuda") for _ in range(rounds)]
+        torch.cuda.synchronize()
+        for i in range(rounds):
+            qkn.norm_quant(xs[i], q)
+            qkn.quant_weight(ww[i % 3], w)
+            if sync:
+                torch.cuda.synchronize()
+            qkn.fp8_linear(q, w, [outs[i]], ws, kernel=kernel)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    want = chain(True)
+    for _ in range(4):
+        for a, b in zip(chain(False), want):
+            assert torch.equal(a, b)
+    assert qkn.read_device_status(ws) == qkn.OK
