@@ -95,16 +95,28 @@ class DecodeStep:
                step_writes_only=True)
         self._host_out_buf.copy_(self._dev_out_buf, non_blocking=True)
 
+    def _read(self) -> tuple:
+        """What the graph reads or writes of the session's."""
+        s = self.session
+        s.ensure_query_buffers(self.batch * self.s_q)    # (other sizes may have come since __init__)
+        return s.q_tilde, s.a_q, s.q_rope_hat
+
     def capture(self) -> None:
-        """Run the step once eagerly (first-call setup in the library), then capture it."""
+        """Run the step once eagerly (first-call setup in the library), then capture it.  The graph keeps the session's
+        weights and buffers of this moment: they live as long as it does, and weights that are loaded later are for
+        steps that are captured later."""
+        s, c = self.session, self.session.cache
+        kept = (c.latent, c.k_rope, c.a_k, c.ak_scratch, s.w_k, s.key_gram, s.gamma_q, s.gamma_k, s.gamma_qr,
+                s.gamma_kr, *self._read())
         stream = torch.cuda.Stream(device=self.session.device)
         stream.wait_stream(torch.cuda.current_stream(self.session.device))
         with torch.cuda.stream(stream):
             self._body()
         stream.synchronize()
-        self.graph = torch.cuda.CUDAGraph()
-        with torch.cuda.graph(self.graph, stream=stream, capture_error_mode="relaxed"):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream, capture_error_mode="relaxed"):
             self._body()
+        self.graph, self.kept = graph, kept
         torch.cuda.current_stream(self.session.device).wait_stream(stream)
 
     def run(self):
@@ -150,7 +162,7 @@ class LayerStep(DecodeStep):
         self.hidden, self.residual = dv["hidden"], dv["residual"]
         self.host_out = (hv["hidden"], hv["residual"])
         # buffers of its own, so that other sizes on the same session leave the captured ones alone, and the
-        # weights that the graph will read, so that they live as long as it does
+        # projections that the graph will read (capture keeps the attention's weights)
         self.gamma_x, self.w_in, self.w_out, self.w_uv = session.gamma_x, session.w_in, session.w_out, session.w_uv
         self.proj_workspace = session.proj_workspace
         self.x8 = Fp8Rows.empty(n, width, dev)
@@ -168,6 +180,9 @@ class LayerStep(DecodeStep):
         self.graph = None
         self.h2d_bytes = in_bytes
         self.d2h_bytes = out_bytes
+
+    def _read(self) -> tuple:
+        return ()                                        # buffers of its own, projections held by __init__
 
     def _body(self) -> None:
         s, d, di = self.session, self.session.dims, self.dev_in

@@ -155,3 +155,34 @@ def test_projections_loaded_again_with_another_width():
         s.project_out(torch.randn((1, heads, 2 * d_v), generator=g).cuda())
     with pytest.raises(ValueError):
         LayerStep(s, 1, 1, 4)
+
+
+def test_a_captured_layer_keeps_the_weights_of_its_capture():
+    """Every weight of the session loaded again, the attention's and the projections': the graph replays with its own."""
+    import weakref
+    inp, s, x, res, gamma, last = build("small_mla_bf16")
+    wl = inp.wl
+    step = LayerStep(s, wl.batch, wl.s_q, inp.block_table.shape[1])
+    fixed = {"slot": inp.token_slots()[last], "pos": inp.token_positions()[last], "block_table": inp.block_table,
+             "seq_lens": inp.seq_lens}
+    for k, v in fixed.items():
+        step.host_in[k].copy_(torch.from_numpy(np.ascontiguousarray(v)))
+    step.host_in["x"].copy_(x)
+    step.host_in["residual"].copy_(res)
+    first = [t.clone() for t in step.run()]
+    names = ("w_k", "key_gram", "gamma_q", "gamma_k", "gamma_qr", "gamma_kr", "w_uv", "gamma_x")
+    held = {k: weakref.ref(getattr(s, k)) for k in names}
+    held.update({w + part: weakref.ref(getattr(getattr(s, w), part)) for w in ("w_in", "w_out")
+                 for part in ("codes", "scale")})
+    width, rows = s.w_in.cols, s.w_in.rows
+    s.load_weights(inp.w_k * 3.0, inp.gamma_q * 0.5, inp.gamma_k + 1.0, inp.gamma_qr * 2.0, inp.gamma_kr * 2.0)
+    s.load_value_weights(inp.w_uv * 2.0)
+    s.load_projections(torch.ones(width), torch.zeros((rows, width)), torch.zeros((width, wl.heads * wl.d_v)))
+    assert [k for k, r in held.items() if r() is None] == []
+    junk = [torch.full_like(r(), 7.0) for r in held.values() for _ in range(2)]
+    hidden, total = step.run()
+    del junk
+    assert s.device_status() == qkn.OK
+    assert torch.equal(total, first[1])
+    # (the key statistics are summed with atomics: equal up to rounding and the codes it moves)
+    assert (hidden.float() - first[0].float()).abs().max() <= 2 ** -4 * first[0].float().abs().max()

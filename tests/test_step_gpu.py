@@ -76,3 +76,33 @@ def test_step_byte_counts():
     assert step.d2h_bytes == field(step.host_out[0].numel() * 4) + field(step.host_out[1].numel() * 4)
     for t in list(step.host_in.values()) + list(step.dev_in.values()):
         assert t.data_ptr() % 256 == 0
+
+
+def test_a_captured_step_keeps_the_weights_and_buffers_of_its_capture():
+    """Weights loaded again and other sizes on the session replace its tensors; the graph's own must not go back to
+    the allocator while it can be replayed."""
+    import weakref
+    inp = make_inputs(WORKLOADS["small_mla_bf16"])
+    wl = inp.wl
+    s = session_from_inputs(inp)
+    last, _, host = _step_inputs(inp)
+    step = DecodeStep(s, wl.batch, wl.s_q, inp.block_table.shape[1], len(last))
+    for k, v in host.items():
+        step.host_in[k].copy_(torch.from_numpy(np.ascontiguousarray(v)).to(step.host_in[k].dtype))
+    s.absorb(inp.q.reshape(-1, wl.heads, wl.d_h)[:1], inp.q_rope.reshape(-1, wl.heads, wl.d_rope)[:1],
+             inp.query_positions().reshape(-1)[:1])           # other sizes between __init__ and the first run
+    assert s.q_tilde.shape[0] == 1
+    first = [t.clone() for t in step.run()]
+    names = ("w_k", "key_gram", "gamma_q", "gamma_k", "gamma_qr", "gamma_kr", "q_tilde", "a_q", "q_rope_hat")
+    held = {k: weakref.ref(getattr(s, k)) for k in names}
+    s.load_weights(inp.w_k * 3.0, inp.gamma_q * 0.5, inp.gamma_k + 1.0, inp.gamma_qr * 2.0, inp.gamma_kr * 2.0)
+    s.absorb(inp.q.reshape(-1, wl.heads, wl.d_h)[:1], inp.q_rope.reshape(-1, wl.heads, wl.d_rope)[:1],
+             inp.query_positions().reshape(-1)[:1])
+    assert [k for k, r in held.items() if r() is None] == []
+    for _ in range(2):                                        # whatever the allocator would hand out again
+        junk = [torch.full_like(r(), 7.0) for r in held.values()]
+    out, lse = step.run()
+    del junk
+    assert s.device_status() == qkn.OK
+    assert (out.float() - first[0].float()).abs().max() <= 2 ** -7 * first[0].float().abs().max()
+    assert (lse - first[1]).abs().max() <= LSE_TOL[wl.dtype]
