@@ -17,6 +17,7 @@ load time, ``qkn_quant_weight``).
 """
 from __future__ import annotations
 
+import weakref
 from typing import Optional
 
 import numpy as np
@@ -42,6 +43,7 @@ class DecodeSession:
         self.w_uv: Optional[torch.Tensor] = None
         self.q_tilde = self.a_q = self.q_rope_hat = None
         self.workspace: Optional[torch.Tensor] = None
+        self._workspaces = []                          # weak references to the ones before, which steps may hold
         self.w_in: Optional[Fp8Weight] = None
         self.w_out: Optional[Fp8Weight] = None
         self.gamma_x: Optional[torch.Tensor] = None
@@ -78,8 +80,9 @@ class DecodeSession:
         self.gamma_x, self.w_in = gamma_x, self._quantised(w_in)
         self.w_out = None if w_out is None else self._quantised(w_out)
         self.q = self.x8 = self.o8 = None              # sized by the weights
-        self.proj_workspace = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
-        workspace_init(self.proj_workspace)
+        if self.proj_workspace is None:                # kept: steps record into it, and an error stays until cleared
+            self.proj_workspace = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)
+            workspace_init(self.proj_workspace)
 
     def check_out_width(self) -> None:
         """load_value_weights may have replaced the weights that load_projections was given w_out for."""
@@ -185,8 +188,11 @@ class DecodeSession:
     def ensure_workspace(self, batch: int, s_q: int) -> torch.Tensor:
         need = decode_workspace_size(self.dims, batch, s_q)
         if self.workspace is None or self.workspace.numel() < need:
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+            old, self.workspace = self.workspace, torch.empty(need, dtype=torch.uint8, device=self.device)
             workspace_init(self.workspace)
+            if old is not None:                        # an error that is recorded there stays until it is cleared
+                self.workspace[:4].copy_(old[:4])
+                self._workspaces = [r for r in self._workspaces if r() is not None] + [weakref.ref(old)]
         return self.workspace
 
     def decode(self, block_table, seq_lens, s_q: int, out=None, lse=None, ak_mode: int = AK_CACHE,
@@ -227,18 +233,20 @@ class DecodeSession:
                   split_event=split_event, step_writes_only=step_writes_only)
         return out_v, lse
 
+    def _status_words(self):
+        """The workspaces whose status words a kernel of the session's or of a step's may write: the decode's, those
+        that it has outgrown but a step still holds, the projections'."""
+        outgrown = [w for w in (r() for r in self._workspaces) if w is not None]
+        return [w for w in (self.workspace, *outgrown, self.proj_workspace) if w is not None] or [None]
+
     def device_status(self) -> int:
-        """The first error that a kernel recorded: the decode's, then the projections'."""
-        status = read_device_status(self.workspace) if self.workspace is not None or self.proj_workspace is None else OK
-        if status == OK and self.proj_workspace is not None:
-            status = read_device_status(self.proj_workspace)
-        return status
+        """The first error that a kernel recorded: the decode's, then the projections'.  The steps of the session
+        record here too."""
+        return next((st for st in map(read_device_status, self._status_words()) if st != OK), OK)
 
     def clear_status(self) -> None:
-        if self.workspace is not None or self.proj_workspace is None:
-            workspace_init(self.workspace)
-        if self.proj_workspace is not None:
-            workspace_init(self.proj_workspace)
+        for w in self._status_words():
+            workspace_init(w)
 
 
 def session_from_inputs(inp, device="cuda", dtype=None) -> DecodeSession:

@@ -186,3 +186,32 @@ def test_a_captured_layer_keeps_the_weights_of_its_capture():
     assert torch.equal(total, first[1])
     # (the key statistics are summed with atomics: equal up to rounding and the codes it moves)
     assert (hidden.float() - first[0].float()).abs().max() <= 2 ** -4 * first[0].float().abs().max()
+
+
+def test_errors_that_a_step_recorded_are_the_session_s():
+    """A step's status words stay visible when the session loads its projections again or grows its workspace, an
+    error that nobody has read yet too, and clear_status clears them all.  (The words are written by hand.)"""
+    inp, s, x, res, gamma, last = build("tiny_f32")
+    step = LayerStep(s, inp.wl.batch, inp.wl.s_q, inp.block_table.shape[1])
+    record = lambda w, code: w[:4].view(torch.int32).fill_(code)
+    rows, width = sum(s.projection_widths()), s.w_in.cols
+    w_out = torch.zeros((width, s.w_out.cols))
+    record(step.proj_workspace, qkn.ERR_TIMEOUT)                 # not read yet
+    s.load_projections(torch.ones(width), torch.zeros((rows, width)), w_out)
+    assert s.device_status() == qkn.ERR_TIMEOUT
+    s.clear_status()
+    assert s.device_status() == qkn.OK
+    record(step.proj_workspace, qkn.ERR_TIMEOUT)                 # recorded by the older step
+    assert s.device_status() == qkn.ERR_TIMEOUT
+    s.clear_status()
+    before = step.workspace
+    record(before, qkn.ERR_BOUNDS)
+    assert s.ensure_workspace(512, 4) is not before
+    assert s.device_status() == qkn.ERR_BOUNDS
+    s.clear_status()
+    assert s.device_status() == qkn.OK and qkn.read_device_status(before) == qkn.OK
+    record(step.workspace, qkn.ERR_TIMEOUT)
+    assert s.device_status() == qkn.ERR_TIMEOUT
+    s.clear_status()
+    del step, before
+    assert s.device_status() == qkn.OK
