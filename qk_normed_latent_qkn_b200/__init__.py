@@ -354,7 +354,9 @@ FP8_GROUP = 128            # columns (and, in a weight, rows) that share a scale
 _E4M3, _FP32 = torch.float8_e4m3fn, torch.float32
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float32: F32}
 _OUT_ARRAYS = tuple(_OutCols * i for i in range(MAX_OUTS + 1))
-_cuda_device, _cuda_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+# (torch's own shortcuts past device and stream objects, where this torch has them)
+_cuda_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_cuda_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
 class Fp8Rows:

@@ -2,6 +2,8 @@
 binding (nothing is launched)."""
 import ctypes
 import os
+import subprocess
+import sys
 from fractions import Fraction
 
 import numpy as np
@@ -263,3 +265,22 @@ def test_fp8_linear_refuses_bad_options(opts):
     rows = _rows(rows=0, codes=None, scale=None)
     assert qkn.raw_library().qkn_fp8_linear_ex(ctypes.byref(rows), ctypes.byref(_weight()), qkn.BF16, 1, arr, P, 256,
                                                ctypes.byref(qkn._LinearOpts(kernel=3)), None) == qkn.OK
+
+
+def test_package_imports_where_torch_lacks_its_private_shortcuts():
+    """As in a torch without CUDA: the package imports, and calls on CPU tensors are refused as ever."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import qk_normed_latent_qkn_b200 as qkn
+try:
+    qkn.norm_quant(torch.zeros((4, 256)), qkn.Fp8Rows.empty(4, 256, "cpu"))
+except qkn.QknError as e:
+    assert e.status == qkn.ERR_INVALID_ARG
+else:
+    raise SystemExit("not refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(qkn.__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
