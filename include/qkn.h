@@ -491,7 +491,8 @@ typedef struct {
 /* qkn_norm_quant — residual addition, RMSNorm and quantisation of n = q->rows rows of d = q->cols values:
  *   h = x, or x + residual rounded to dtype and written to residual_out;
  *   y = h * gamma / sqrt(mean(h^2) + eps), or y = h without gamma (no norm);
- *   per row and block of 128 columns: scale = max(max|y| / 448, 2^-100), code = the fp32 quotient
+ *   per row and block of 128 columns: scale = max(max|y| / 448, 2^-100), the division being a product
+ *   with 1 / 448 rounded to fp32 (as torch divides by a number on a GPU), code = the fp32 quotient
  *   y / scale, rounded to the nearest e4m3 (ties to the even code).
  * fp32 arithmetic; the sum of squares must stay in fp32's range.  A NaN makes its block of codes (with
  * gamma: its row) NaN, an infinity without gamma its block; other rows are not touched by it.

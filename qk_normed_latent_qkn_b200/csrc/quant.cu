@@ -21,7 +21,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax / kFp8Top, kFp8Least); }
+// (times the rounded reciprocal, within 1.75 * 2^-24 of the quotient: what a tensor divided by a number is in
+// torch on a GPU, so that scales and codes agree with weights that were quantised there)
+__device__ __forceinline__ float scale_of(float amax) { return max_nan(amax * (1.f / kFp8Top), kFp8Least); }
 
 // v / s for the values of a block from r = 1 / s: q = v r, corrected by its remainder, v - q s, times r
 // (Markstein's division).  It gives the code that the correctly rounded quotient gives, for every v and s: before

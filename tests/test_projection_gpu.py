@@ -459,6 +459,12 @@ def quotient_codes(y, scale):
     return (y.float() / scale).to(torch.float8_e4m3fn).float()
 
 
+def quotient_scale(amax):
+    """A block's scale by its definition in fp32, on the host: the largest magnitude times the rounded 1 / 448."""
+    return torch.clamp(torch.as_tensor(amax, dtype=torch.float32).cpu() * torch.tensor(1 / 448, dtype=torch.float32),
+                       min=2.0 ** -100)
+
+
 def assert_codes(codes, y, scale):
     got, want = codes.float().cpu(), quotient_codes(y.cpu(), scale.cpu())
     assert torch.equal(torch.isnan(got), torch.isnan(want))
@@ -497,7 +503,7 @@ def test_weight_codes_are_the_rounded_quotients(n, k, dtype):
         q = qkn.Fp8Weight.empty(n, k)
         qkn.quant_weight(w.cuda(), q)
         per = np.array([[w[i:i + 128, j:j + 128].float().abs().max() for j in range(0, k, 128)] for i in range(0, n, 128)])
-        scale = torch.from_numpy(per) / 448
+        scale = quotient_scale(per)
         assert torch.equal(q.scale.cpu(), scale)
         of = scale.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
         assert_codes(q.codes[:, :k], w, of)
@@ -513,7 +519,7 @@ def test_row_codes_are_the_rounded_quotients(n, d, dtype):
         of = lambda q: q.scale[:, :m].t().repeat_interleave(128, 1)[:, :d]
         assert_codes(q.codes[:, :d], x, of(q))
         per = torch.stack([x[:, j:j + 128].float().abs().amax(1) for j in range(0, d, 128)])
-        assert torch.equal(q.scale[:, :m].cpu(), per.cpu() / 448)
+        assert torch.equal(q.scale[:, :m].cpu(), quotient_scale(per))
         if dtype == torch.float32:
             q, _, y = run_norm(x, torch.ones(d, device="cuda"), want_y=True)
             assert_codes(q.codes[:, :d], y, of(q))
@@ -629,3 +635,20 @@ def test_every_kernel_in_a_chain_through_rewritten_buffers(m, kernel):
         for a, b in zip(chain(False), want):
             assert torch.equal(a, b)
     assert qkn.read_device_status(ws) == qkn.OK
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_codes_and_scales_are_those_of_torch_on_the_gpu(dtype):
+    """Weights and rows quantised with elementary torch operations on the GPU, to the bit."""
+    for x in (hidden(300, 900, dtype, 1), beside_midpoints(140, 640, dtype, 2).cuda()):
+        n, d = x.shape
+        q, _, _ = run_norm(x)
+        blocks = torch.nn.functional.pad(x.float(), (0, -d % 128)).view(n, -1, 128)
+        scale = (blocks.abs().amax(-1) / 448.0).clamp_min(2.0 ** -100)
+        codes = (blocks / scale[..., None]).to(torch.float8_e4m3fn).view(n, -1)[:, :d]
+        assert torch.equal(q.scale[:, :n], scale.t()) and torch.equal(q.codes[:, :d].float(), codes.float())
+        w = qkn.Fp8Weight.empty(n, d)
+        qkn.quant_weight(x, w)
+        scale = torch.stack([blocks[i:i + 128].abs().amax((0, 2)) / 448.0 for i in range(0, n, 128)])
+        codes = (blocks / scale.repeat_interleave(128, 0)[:n][..., None]).to(torch.float8_e4m3fn).view(n, -1)[:, :d]
+        assert torch.equal(w.scale, scale) and torch.equal(w.codes[:, :d].float(), codes.float())
