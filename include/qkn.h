@@ -513,7 +513,8 @@ QKN_EXPORT qkn_status qkn_quant_weight(qkn_dtype dtype, const void* w, const qkn
 
 /* qkn_fp8_linear — out = A W^T for rows and a weight in 8 bits:
  *   out[i, n] = sum over blocks b of scale_a[b, i] scale_w[n / 128, b] sum_{k in b} a[i, k] w[n, k],
- * products and sums in fp32, rounded once to out_dtype.  The columns go to n_outs <= QKN_MAX_OUTS
+ * products and sums in fp32, rounded once to out_dtype (the two scales are multiplied first: blocks for which
+ * that product is below 2^-126 lose accuracy, from 2^128 on they give infinities or NaN).  The columns go to n_outs <= QKN_MAX_OUTS
  * destinations in order (their widths add up to w->rows), so that one product fills, say, q, q^R, c and
  * k^R where qkn_append_absorb reads them.
  *   a->cols == w->cols;  workspace >= 256 bytes, 256-byte aligned, initialised with qkn_workspace_init:

@@ -142,10 +142,11 @@ __device__ __forceinline__ void write_box(const Fp8LinearArgs& p, const uint8_t*
 // A pair's tile halves what each SM has to fetch of the weight (32 KB a block of K for 256 x 256 outputs,
 // and the L2 link of an SM brings about 64 bytes a cycle).  The scales of a block enter in fp32, so every
 // block's sums leave tensor memory: the MMAs of a block (512 cycles of an SM at 256 columns) fill one
-// accumulator while eight warps promote the other.  That promotion bounds the kernel: 835 cycles a block
-// on a B200, 683 without its FMAs, 607 without it.  8192 x 25152 x 4096: 765 to 900 us, 1.9 to 2.2 PFLOP/s
-// at 1.4 to 1.6 GHz, the power cap's doing; 4096 x 4096 x 16384: 270 to 315 us.  Sixteen promoting warps
-// were slower (they leave 96 registers each), as were half-width accumulators and packed FMAs.
+// accumulator while eight warps promote the other.  The promotion's latency bounds the kernel, not a unit's rate: 835
+// cycles a block on a B200, 683 without its FMAs, 607 without it, while the tensor pipe is 58 % busy, the issue
+// slots 53 % and the FMA pipe 33 %.  8192 x 25152 x 4096: 890 to 940 us, 1.8 to 1.9 PFLOP/s at 1.4 GHz, the
+// power cap's doing (765 us in bursts at 1.6); 4096 x 4096 x 16384: 295 to 315 us.  Sixteen promoting warps were
+// slower (they leave 96 registers each), as were half-width accumulators and packed FMAs.
 constexpr int kPairM = 256;                     // rows of a pair's tile
 constexpr int kPairWarps = 8;                   // epilogue warps, each 32 rows x half the tile's columns
 constexpr int kPairThreads = 64 + 32 * kPairWarps;
@@ -450,8 +451,8 @@ struct SplitBars {
 };
 
 // Bound by memory or, in short calls, by the chain of one load, MMA, promotion and join: 32 x 25152 x 4096
-// takes 22 us on a B200 (103 MB of weight; 7 TB/s once it streams, 5 us to start and end), 64 x 4096 x 16384
-// 19, 1 x 576 x 2048 3.7.  Splitting K over a cluster needs no workspace and no atomics, and the parts are
+// takes 21 us on a B200 (103 MB of weight; 7 TB/s once it streams, 5 us to start and end), 1 x 576 x 2048 3.6, and
+// 64 x 4096 x 16384 18.4 (256 CTAs on 148 SMs: 108 of these carry two).  Splitting K over a cluster needs no workspace and no atomics, and the parts are
 // added in rank order: the same bits every time.
 // One tile: 128 columns of the product for NT rows.  Cluster rank r takes the r-th part of K's blocks.
 // Warps: 0 producer, 1 MMA, 2 on: epilogue.
@@ -743,8 +744,9 @@ int clusters_of(int size, int sms) {
 // CTAs of a split kernel that the device holds at once in clusters of `split` (2, 4 or 8); a cluster too many
 // costs a whole wave (32 x 9472 x 4096: 17.8 us in 74 clusters of 4, 11.1 in 74 of 2).  The runtime counts one
 // CTA of a kernel with tensor memory per SM.  Where two run there, a cluster needs split / 2 SMs at best and
-// split at worst: two thirds of the way between the two counts (285 and 256 CTAs for 4 and 8; B200 runs took 272
-// but not 288, and 264 but not 280, without another wave).  Asked once per device.
+// split at worst: an estimate two thirds of the way between the two counts, 285 and 256 CTAs for 4 and 8 (B200 runs
+// took 272 but not 288, and 264 but not 280, without another wave: for clusters of 8 it is on the safe side).
+// Asked once per device.
 template <int NT, typename O>
 int resident_of(int split, int dev, int sms) {
   static std::atomic<int> known[64][3];
@@ -811,14 +813,16 @@ cudaError_t launch_split(const Fp8LinearArgs& a, int dev, int sms, cudaStream_t 
 // (nanoseconds for a start, for a tile's start and end, and for a block of K) are from B200 runs: the
 // estimates are within a fifth of the times below, and the choice falls on the shortest but for near ties.
 //   rows x columns x K       pairs of 256   pairs of 128   split
-//   128 x 25152 x 4096            38 us          38 us      37 us
-//   256 x 25152 x 4096            39             38         55
-//   512 x  4096 x 16384           62             46         52
-//   256 x  4096 x 16384           60             45         30
-//   1024 x 4096 x 16384           66            103        100
-//   2048 x  576 x 4096            20             15         18
-//   333 x  1000 x 1960            16             10         7.5
-//   4096 x 4096 x 16384          303            374          -
+//    65 x 25152 x 4096            37 us          36 us      32 us
+//   128 x 25152 x 4096            38             37         35
+//   256 x 25152 x 4096            39             38         50
+//   512 x  4096 x 16384           63             47         46
+//   256 x  4096 x 16384           63             46         27
+//   1024 x 4096 x 16384           68             99         94
+//   2048 x  576 x 4096            21             15         18
+//   333 x  1000 x 1960            14             10         7.4
+//   8192 x 8000 x 512             60             68          -
+//   4096 x 4096 x 16384          306            384          -
 template <typename O>
 int choose(int64_t m, int64_t n, int blocks, int dev, int sms) {
   const int64_t row_tiles = ceil_div(m, kPairM);

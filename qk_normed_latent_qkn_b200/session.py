@@ -14,6 +14,9 @@ With ``load_projections`` the session starts from hidden states and ends in
 them: the layer's projections around the attention run in 8 bits
 (``qkn_norm_quant``, ``qkn_fp8_linear``; weights quantised on the device at
 load time, ``qkn_quant_weight``).
+
+A session's calls share its buffers: they run on one stream, or one after the
+other.
 """
 from __future__ import annotations
 
@@ -104,7 +107,8 @@ class DecodeSession:
     def project(self, x, residual=None):
         """Hidden states [n, D] -> q [n, H, d_h], q^R [n, H, d_R], c [n, r], k^R [n, d_R] (raw, as append and absorb
         take them).  ``residual`` (a device tensor [n, D]) is added first and takes the sum.  The output buffers are
-        reused while n stays the same."""
+        reused while n stays the same and replaced when it changes, so a graph of the caller's that captured this call
+        may be replayed only while no other size has come since (LayerStep has buffers of its own)."""
         d, dt, dev = self.dims, self.dims.torch_dtype, self.device
         if self.w_in is None:
             raise RuntimeError("project needs load_projections first")
