@@ -47,6 +47,7 @@ class DecodeSession:
         self.q_tilde = self.a_q = self.q_rope_hat = None
         self.workspace: Optional[torch.Tensor] = None
         self._workspaces = []                          # weak references to the ones before, which steps may hold
+        self._kept = []                                # the ones before that were outgrown inside a capture
         self.w_in: Optional[Fp8Weight] = None
         self.w_out: Optional[Fp8Weight] = None
         self.gamma_x: Optional[torch.Tensor] = None
@@ -195,7 +196,10 @@ class DecodeSession:
             old, self.workspace = self.workspace, torch.empty(need, dtype=torch.uint8, device=self.device)
             workspace_init(self.workspace)
             if old is not None:                        # an error that is recorded there stays until it is cleared
-                self.workspace[:4].copy_(old[:4])
+                if torch.cuda.is_current_stream_capturing():
+                    self._kept.append(old)             # (a copy would run again with every replay)
+                else:
+                    self.workspace[:4].copy_(old[:4])
                 self._workspaces = [r for r in self._workspaces if r() is not None] + [weakref.ref(old)]
         return self.workspace
 

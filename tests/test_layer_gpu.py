@@ -215,3 +215,24 @@ def test_errors_that_a_step_recorded_are_the_session_s():
     s.clear_status()
     del step, before
     assert s.device_status() == qkn.OK
+
+
+def test_a_workspace_outgrown_inside_a_capture_is_not_read_by_the_replays():
+    s = session_from_inputs(make_inputs(WORKLOADS["tiny_f32"]))
+    s.ensure_workspace(1, 1)
+    size = s.workspace.numel()
+    s.workspace[:4].view(torch.int32).fill_(qkn.ERR_BOUNDS)      # recorded, and not read yet
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.ensure_workspace(512, 4)
+    assert s.workspace.numel() > size
+    junk = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    graph.replay()
+    torch.cuda.synchronize()
+    del junk
+    assert s.device_status() == qkn.ERR_BOUNDS
+    s.clear_status()
+    assert s.device_status() == qkn.OK
+    graph.replay()
+    assert s.device_status() == qkn.OK
