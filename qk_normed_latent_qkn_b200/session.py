@@ -47,13 +47,19 @@ class DecodeSession:
         self.q_tilde = self.a_q = self.q_rope_hat = None
         self.workspace: Optional[torch.Tensor] = None
         self._workspaces = []                          # weak references to the ones before, which steps may hold
-        self._kept = []                                # the ones before that were outgrown inside a capture
+        self._kept = {}                                # what captured calls use, by id
         self.w_in: Optional[Fp8Weight] = None
         self.w_out: Optional[Fp8Weight] = None
         self.gamma_x: Optional[torch.Tensor] = None
         self.x8 = self.o8 = None                       # the projections' inputs in 8 bits
         self.q = self.q_rope = self.c_new = self.k_rope_new = None
         self.proj_workspace: Optional[torch.Tensor] = None
+
+    def _keep(self, *used) -> None:
+        """Buffers and weights that a call is about to use.  If a graph captures the call it holds their addresses, so
+        they stay when other sizes or other weights take their place here."""
+        if torch.cuda.is_current_stream_capturing():
+            self._kept.update((id(t), t) for t in used)
 
     # ------------------------------------------------------------ weights
     def load_weights(self, w_k, gamma_q, gamma_k, gamma_qr, gamma_kr) -> None:
@@ -108,8 +114,7 @@ class DecodeSession:
     def project(self, x, residual=None):
         """Hidden states [n, D] -> q [n, H, d_h], q^R [n, H, d_R], c [n, r], k^R [n, d_R] (raw, as append and absorb
         take them).  ``residual`` (a device tensor [n, D]) is added first and takes the sum.  The output buffers are
-        reused while n stays the same and replaced when it changes, so a graph of the caller's that captured this call
-        may be replayed only while no other size has come since (LayerStep has buffers of its own)."""
+        reused while n stays the same."""
         d, dt, dev = self.dims, self.dims.torch_dtype, self.device
         if self.w_in is None:
             raise RuntimeError("project needs load_projections first")
@@ -119,6 +124,7 @@ class DecodeSession:
             self.x8 = Fp8Rows.empty(n, self.w_in.cols, dev)
             self.q, self.q_rope, self.c_new, self.k_rope_new = (
                 torch.empty((n, w), dtype=dt, device=dev) for w in self.projection_widths())
+        self._keep(self.x8, self.q, self.q_rope, self.c_new, self.k_rope_new, self.gamma_x, self.w_in)
         norm_quant(x, self.x8, gamma=self.gamma_x, eps=d.eps, residual=residual, residual_out=residual)
         fp8_linear(self.x8, self.w_in, (self.q, self.q_rope, self.c_new, self.k_rope_new), self.proj_workspace)
         return (self.q.view(n, d.num_heads, d.d_h), self.q_rope.view(n, d.num_heads, d.d_rope), self.c_new,
@@ -144,6 +150,7 @@ class DecodeSession:
             self.o8 = Fp8Rows.empty(n, self.w_out.cols, self.device)
         if out is None:
             out = torch.empty((n, self.w_out.rows), dtype=self.dims.torch_dtype, device=self.device)
+        self._keep(self.o8, self.w_out)
         norm_quant(rows, self.o8)
         fp8_linear(self.o8, self.w_out, (out,), self.proj_workspace)
         return out
@@ -153,6 +160,7 @@ class DecodeSession:
         """Append tokens (host or device arrays) in chunks of ``chunk`` tokens."""
         dt, dev = self.dims.torch_dtype, self.device
         n = int(c.shape[0])
+        self._keep(self.w_k, self.key_gram, self.gamma_kr)
         for t0 in range(0, n, chunk):
             sl = slice(t0, min(n, t0 + chunk))
             append(self.dims, self.cache, to_device(c[sl], dt, dev), to_device(k_rope_raw[sl], dt, dev),
@@ -167,6 +175,7 @@ class DecodeSession:
         q = to_device(q, dt, dev)
         q_rope = to_device(q_rope, dt, dev)
         self.ensure_query_buffers(q.shape[0])
+        self._keep(self.w_k, self.gamma_q, self.gamma_k, self.gamma_qr)
         absorb_query(d, q, q_rope, to_device(pos, torch.int32, dev), self.w_k, self.gamma_q, self.gamma_k,
                      self.gamma_qr, self.q_tilde, self.a_q, self.q_rope_hat)
 
@@ -175,6 +184,7 @@ class DecodeSession:
         d, dt, dev = self.dims, self.dims.torch_dtype, self.device
         q = to_device(q, dt, dev)
         self.ensure_query_buffers(q.shape[0])
+        self._keep(self.w_k, self.key_gram, self.gamma_q, self.gamma_k, self.gamma_qr, self.gamma_kr)
         append_absorb(d, self.cache, to_device(c, dt, dev), to_device(k_rope_raw, dt, dev),
                       to_device(slot, torch.int32, dev), to_device(pos, torch.int32, dev), q,
                       to_device(q_rope, dt, dev), to_device(qpos, torch.int32, dev), self.w_k, self.key_gram,
@@ -188,6 +198,7 @@ class DecodeSession:
             self.q_tilde = torch.empty((n_q, d.num_heads, d.r_kv), dtype=dt, device=dev)
             self.a_q = torch.empty((n_q, d.num_heads), dtype=torch.float32, device=dev)
             self.q_rope_hat = torch.empty((n_q, d.num_heads, d.d_rope), dtype=dt, device=dev)
+        self._keep(self.q_tilde, self.a_q, self.q_rope_hat)
 
     # ------------------------------------------------------------ decode
     def ensure_workspace(self, batch: int, s_q: int) -> torch.Tensor:
@@ -197,10 +208,11 @@ class DecodeSession:
             workspace_init(self.workspace)
             if old is not None:                        # an error that is recorded there stays until it is cleared
                 if torch.cuda.is_current_stream_capturing():
-                    self._kept.append(old)             # (a copy would run again with every replay)
+                    self._keep(old)                    # (a copy would run again with every replay)
                 else:
                     self.workspace[:4].copy_(old[:4])
                 self._workspaces = [r for r in self._workspaces if r() is not None] + [weakref.ref(old)]
+        self._keep(self.workspace)
         return self.workspace
 
     def decode(self, block_table, seq_lens, s_q: int, out=None, lse=None, ak_mode: int = AK_CACHE,
@@ -215,6 +227,7 @@ class DecodeSession:
             out = torch.empty((batch, s_q, d.num_heads, d.r_kv), dtype=d.torch_dtype, device=dev)
         if lse is None:
             lse = torch.empty((batch, s_q, d.num_heads), dtype=torch.float32, device=dev)
+        self._keep(self.q_tilde, self.a_q, self.q_rope_hat)
         decode(d, self.cache, self.q_tilde, self.a_q, self.q_rope_hat, bt, sl, s_q, ws, out, lse,
                ak_mode=ak_mode, kernel=kernel, max_ctas=max_ctas, head_tile=head_tile, wait_limit=wait_limit,
                split_event=split_event, step_writes_only=step_writes_only, test_withhold_ak=test_withhold_ak,
@@ -236,6 +249,7 @@ class DecodeSession:
             out_v = torch.empty((batch, s_q, d.num_heads, self.w_uv.shape[-1]), dtype=d.torch_dtype, device=dev)
         if lse is None:
             lse = torch.empty((batch, s_q, d.num_heads), dtype=torch.float32, device=dev)
+        self._keep(self.w_uv, self.q_tilde, self.a_q, self.q_rope_hat)
         decode_up(d, self.cache, self.q_tilde, self.a_q, self.q_rope_hat, bt, sl, s_q, self.w_uv, ws, out_v, lse,
                   ak_mode=ak_mode, kernel=kernel, max_ctas=max_ctas, head_tile=head_tile, wait_limit=wait_limit,
                   split_event=split_event, step_writes_only=step_writes_only)

@@ -236,3 +236,43 @@ def test_a_workspace_outgrown_inside_a_capture_is_not_read_by_the_replays():
     assert s.device_status() == qkn.OK
     graph.replay()
     assert s.device_status() == qkn.OK
+
+
+def test_session_calls_in_a_graph_of_the_caller_s():
+    """The session's calls captured by the caller, then other sizes, other weights and a larger workspace on the
+    session: the graph replays with what it captured, and none of that went back to the allocator."""
+    import weakref
+    inp, s, x, res, gamma, last = build("small_mla_bf16")
+    wl = inp.wl
+    slot, pos = (torch.from_numpy(np.ascontiguousarray(v)).cuda() for v in
+                 (inp.token_slots()[last].astype(np.int32), inp.token_positions()[last].astype(np.int32)))
+    bt, sl = torch.from_numpy(inp.block_table).cuda(), torch.from_numpy(inp.seq_lens).cuda()
+
+    def layer():
+        s.prepare_hidden(x, slot, pos)
+        return s.project_out(s.decode_up(bt, sl, wl.s_q)[0])
+
+    want = layer().clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hidden = layer()
+    names = ("w_k", "key_gram", "gamma_q", "gamma_k", "gamma_qr", "gamma_kr", "w_uv", "gamma_x", "q", "q_rope", "c_new",
+             "k_rope_new", "q_tilde", "a_q", "q_rope_hat", "workspace")
+    held = {k: weakref.ref(getattr(s, k)) for k in names}
+    held.update({w + part: weakref.ref(getattr(getattr(s, w), part)) for w in ("w_in", "w_out", "x8", "o8")
+                 for part in ("codes", "scale")})
+    width, rows = s.w_in.cols, s.w_in.rows
+    s.load_weights(inp.w_k * 3.0, inp.gamma_q * 0.5, inp.gamma_k + 1.0, inp.gamma_qr * 2.0, inp.gamma_kr * 2.0)
+    s.load_value_weights(inp.w_uv * 2.0)
+    s.load_projections(torch.ones(width), torch.zeros((rows, width)), torch.zeros((width, wl.heads * wl.d_v)))
+    s.ensure_query_buffers(1)
+    s.project(x[:1])
+    s.ensure_workspace(512, 4)
+    assert [k for k, r in held.items() if r() is None] == []
+    hidden.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert s.device_status() == qkn.OK
+    # (the key statistics are summed with atomics: equal up to rounding and the codes it moves)
+    assert (hidden.float() - want.float()).abs().max() <= 2 ** -4 * want.float().abs().max()
