@@ -87,8 +87,8 @@ class DecodeSession:
             raise ValueError("w_in is [H d_h + H d_R + r + d_R, D], gamma_x [D]")
         if w_out is not None and (self.w_uv is None or w_out.shape[1] != d.num_heads * self.w_uv.shape[-1]):
             raise ValueError("w_out is [D, H d_v] for the value weights loaded before")
-        self.gamma_x, self.w_in = gamma_x, self._quantised(w_in)
-        self.w_out = None if w_out is None else self._quantised(w_out)
+        w_in, w_out = self._quantised(w_in), None if w_out is None else self._quantised(w_out)
+        self.gamma_x, self.w_in, self.w_out = gamma_x, w_in, w_out
         self.q = self.x8 = self.o8 = None              # sized by the weights
         if self.proj_workspace is None:                # kept: steps record into it, and an error stays until cleared
             self.proj_workspace = torch.empty(WORKSPACE_BYTES, dtype=torch.uint8, device=dev)

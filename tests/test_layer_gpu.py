@@ -276,3 +276,25 @@ def test_session_calls_in_a_graph_of_the_caller_s():
     assert s.device_status() == qkn.OK
     # (the key statistics are summed with atomics: equal up to rounding and the codes it moves)
     assert (hidden.float() - want.float()).abs().max() <= 2 ** -4 * want.float().abs().max()
+
+
+class _Broken:
+    """Weights whose shape is right and whose values cannot be had."""
+
+    def __init__(self, shape):
+        self.shape = shape
+
+    def __array__(self, *args, **kwargs):
+        raise OSError("unreadable")
+
+
+def test_projections_that_fail_to_load_leave_the_old_ones():
+    inp, s, x, res, gamma, last = build("tiny_f32")
+    want = [t.clone() for t in s.project(x)]
+    rows, width = sum(s.projection_widths()), 64
+    before = (s.gamma_x, s.w_in, s.w_out)
+    with pytest.raises(OSError):
+        s.load_projections(torch.ones(width), torch.zeros((rows, width)), _Broken((width, s.w_out.cols)))
+    assert all(a is b for a, b in zip(before, (s.gamma_x, s.w_in, s.w_out)))
+    for a, b in zip(s.project(x), want):
+        assert torch.equal(a, b)
