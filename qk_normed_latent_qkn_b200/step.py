@@ -130,7 +130,8 @@ class DecodeStep:
 
 class LayerStep(DecodeStep):
     """One attention layer's decode step: row b s_q + j of ``x`` and ``residual`` is the j-th new token of sequence b.
-    ``run`` returns pinned (hidden, residual): the layer's output [n, D] and x + residual, which the next layer adds."""
+    ``run`` returns pinned (hidden, residual): the layer's output [n, D] and x + residual, which the next layer takes
+    as its ``x`` and ``residual`` (a stack of steps passes both through these host buffers)."""
 
     NAMES = ("x", "residual", "slot", "pos", "block_table", "seq_lens")
 
